@@ -462,6 +462,120 @@ nvfp4_status nvfp4_dequant_batched(int count, const uint8_t* const* codes,
                                    nvfp4_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Products with the solved weights: Y = X Q^T                               */
+/* ------------------------------------------------------------------------ */
+/* "Replay the Curvature", Abstract, NVFP4 sentence and title (inference): a
+ * solved layer answers from its codes and scales as the quantize call wrote
+ * them, Q = e2m1(code) * e4m3(scale) * s_g, without a dequantised copy.
+ *
+ * X       : n_tok x d_in, bf16 or fp32 (x_dtype), 16-byte aligned.
+ * codes, scales, global_scale : of a d_out x d_in matrix, as written by the
+ *           quantize call.
+ * Y       : n_tok x d_out, bf16 or fp32 (y_dtype, its own choice), fully
+ *           written; must not overlap X.  d_in == 0 gives zeros.
+ * The products e2m1 * e4m3 are exact, their sums with X are fp32, and Y is
+ * rounded once; bf16 and fp32 tokens are used at all their bits.  NaN and
+ * infinite tokens behave as in the plain product and stay in their row.  Made
+ * for few tokens, where the weights' bytes bound the product; any n_tok is
+ * right.  No workspace, no status word.
+ * d_out, n_tok <= 2^22, d_in <= 2^17 (NVFP4_ERR_SHAPE beyond). */
+nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const uint8_t* codes,
+                        const uint8_t* scales, const float* global_scale, int64_t d_out,
+                        int64_t d_in, void* Y, nvfp4_dtype y_dtype, nvfp4_stream_t stream);
+
+/* The gated pair of a feed-forward layer in one pass:
+ *   Y = silu(X Qg^T) * (X Qu^T),  silu(g) = g / (1 + exp(-g)),
+ * element by element in fp32, rounded once.  Both matrices are d_out x d_in;
+ * everything else as nvfp4_gemv. */
+nvfp4_status nvfp4_gemv_swiglu(const void* X, nvfp4_dtype x_dtype, int64_t n_tok,
+                               const uint8_t* gate_codes, const uint8_t* gate_scales,
+                               const float* gate_global_scale, const uint8_t* up_codes,
+                               const uint8_t* up_scales, const float* up_global_scale,
+                               int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype y_dtype,
+                               nvfp4_stream_t stream);
+
+/* Experts per call of the products by expert and of the routing calls. */
+#define NVFP4_MAX_EXPERTS 1024
+
+/* The same products by expert, over rows sorted by expert (nvfp4_moe_sort):
+ * row r with offsets[e] <= r < offsets[e+1] is multiplied by expert e's
+ * matrix.  Only the matrices of experts that have rows are read.
+ * offsets : device, n_experts + 1 ascending row offsets (values outside
+ *           0..n_rows are cut to it).
+ * codes, scales, global_scales : the experts' matrices one after another
+ *           (n_experts x d_out x d_in/2, n_experts x d_out x d_in/16, and one
+ *           fp32 per expert).
+ * rows    : device, the row of X that each sorted row reads (n_rows entries;
+ *           one outside 0..n_x-1 reads as a row of zeros), or NULL: X holds
+ *           the sorted rows themselves (n_x == n_rows).
+ * X       : n_x x d_in.   Y: n_rows x d_out; rows outside every expert (before
+ *           offsets[0], from offsets[n_experts] on) are left as they were.
+ * n_experts <= NVFP4_MAX_EXPERTS, n_x and n_rows <= 2^22 (NVFP4_ERR_SHAPE). */
+nvfp4_status nvfp4_gemv_experts(const void* X, nvfp4_dtype x_dtype, int64_t n_x,
+                                const int32_t* rows, const int32_t* offsets, int64_t n_experts,
+                                int64_t n_rows, const uint8_t* codes, const uint8_t* scales,
+                                const float* global_scales, int64_t d_out, int64_t d_in, void* Y,
+                                nvfp4_dtype y_dtype, nvfp4_stream_t stream);
+nvfp4_status nvfp4_gemv_swiglu_experts(
+    const void* X, nvfp4_dtype x_dtype, int64_t n_x, const int32_t* rows, const int32_t* offsets,
+    int64_t n_experts, int64_t n_rows, const uint8_t* gate_codes, const uint8_t* gate_scales,
+    const float* gate_global_scales, const uint8_t* up_codes, const uint8_t* up_scales,
+    const float* up_global_scales, int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype y_dtype,
+    nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Tokens by expert and back                                                 */
+/* ------------------------------------------------------------------------ */
+/* "Replay the Curvature", Abstract: in a mixture-of-experts layer every expert
+ * is its own linear layer with its own Hessian, so its calibration tokens have
+ * to lie together; and a solved layer's experts answer rows that go back to
+ * their tokens.
+ *
+ * nvfp4_moe_sort: a stable counting sort of the slots s = t * top_k + j (token
+ * t's j-th choice) by expert.
+ * expert_ids : n_tok x top_k ids, int32 or int64 (id_bytes 4 or 8); a slot
+ *            whose id is outside 0..n_experts-1 (a padded token's -1) has no
+ *            expert and is left out.  A token may name an expert twice.
+ * offsets  : n_experts + 1 out; expert e's rows are offsets[e]..offsets[e+1]-1,
+ *            in the order of their slots.  offsets[n_experts] rows in all.
+ * rows     : n_tok * top_k out; the token of each sorted row, -1 from
+ *            offsets[n_experts] on.
+ * position : n_tok * top_k out; the sorted row of each slot, -1 for a slot
+ *            without an expert.
+ * Only the stream orders calls: no state is kept between them.
+ * top_k is 1..NVFP4_MAX_EXPERTS, n_experts <= NVFP4_MAX_EXPERTS, n_tok <= 2^26
+ * and n_tok * top_k <= 2^30 (NVFP4_ERR_SHAPE; also for the calls below, with
+ * d <= 2^17).  No output may overlap another array of the call. */
+nvfp4_status nvfp4_moe_sort(const void* expert_ids, int id_bytes, int64_t n_tok, int64_t top_k,
+                            int64_t n_experts, int32_t* offsets, int32_t* rows,
+                            int32_t* position, nvfp4_stream_t stream);
+
+/* Xs[position[t, j]] = X[t]: X is n_tok x d, Xs n_tok * top_k x d, both of
+ * dtype.  Rows of Xs that no slot names are left as they were.  Entries of
+ * position outside 0..n_tok*top_k-1 name no row (here and below). */
+nvfp4_status nvfp4_moe_gather(const void* X, nvfp4_dtype dtype, const int32_t* position,
+                              int64_t n_tok, int64_t top_k, int64_t d, void* Xs,
+                              nvfp4_stream_t stream);
+
+/* Y[t] = sum_j weights[t, j] * Ys[position[t, j]], summed in fp32 in the order
+ * of j and rounded once; a token without rows gives zeros.  Ys is
+ * n_tok * top_k x d of s_dtype, Y n_tok x d of y_dtype, weights n_tok x top_k
+ * fp32 or NULL for 1.  Without weights this is the gradient of
+ * nvfp4_moe_gather: dX from dXs. */
+nvfp4_status nvfp4_moe_combine(const void* Ys, nvfp4_dtype s_dtype, const int32_t* position,
+                               const float* weights, int64_t n_tok, int64_t top_k, int64_t d,
+                               void* Y, nvfp4_dtype y_dtype, nvfp4_stream_t stream);
+
+/* The gradient of nvfp4_moe_combine: dYs[position[t, j]] = weights[t, j] dY[t]
+ * and dweights[t, j] = <dY[t], Ys[position[t, j]]> (fp32; 0 for a slot without
+ * a row).  dY, Ys and dYs are of dtype.  Rows of dYs that no slot names are
+ * left as they were.  dYs must not overlap dY or Ys. */
+nvfp4_status nvfp4_moe_combine_backward(const void* dY, const void* Ys, nvfp4_dtype dtype,
+                                        const int32_t* position, const float* weights,
+                                        int64_t n_tok, int64_t top_k, int64_t d, void* dYs,
+                                        float* dweights, nvfp4_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics: launch accounting and per-phase device timing                */
 /* (measurement support; the paper has no counterpart)                       */
 /* ------------------------------------------------------------------------ */

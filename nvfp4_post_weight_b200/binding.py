@@ -6,6 +6,7 @@ built, importing the calls raises: there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -116,6 +117,16 @@ def _load(path):
                                vp], i32),
         "nvfp4_layer_error_workspace_size": ([i64, i64], sz),
         "nvfp4_layer_error": ([vp, i32, vp, vp, vp, vp, i64, i64, vp, vp, sz, vp], i32),
+        "nvfp4_gemv": ([vp, i32, i64, vp, vp, vp, i64, i64, vp, i32, vp], i32),
+        "nvfp4_gemv_swiglu": ([vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp], i32),
+        "nvfp4_gemv_experts": ([vp, i32, i64, vp, vp, i64, i64, vp, vp, vp, i64, i64, vp, i32, vp],
+                               i32),
+        "nvfp4_gemv_swiglu_experts": (
+            [vp, i32, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp], i32),
+        "nvfp4_moe_sort": ([vp, i32, i64, i64, i64, vp, vp, vp, vp], i32),
+        "nvfp4_moe_gather": ([vp, i32, vp, i64, i64, i64, vp, vp], i32),
+        "nvfp4_moe_combine": ([vp, i32, vp, vp, i64, i64, i64, vp, i32, vp], i32),
+        "nvfp4_moe_combine_backward": ([vp, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp], i32),
         "nvfp4_launch_count": ([], ctypes.c_longlong),
         "nvfp4_debug_build": ([], i32),
         "nvfp4_set_wait_limit_ns": ([ctypes.c_ulonglong], i32),
@@ -610,3 +621,168 @@ def nvfp4_layer_error_batched(Ws, codes, scales, global_scales, Hs, errs, ws, st
         n, _ptrs(Ws), _dtype_code(Ws[0]) if n else 0, _ptrs(codes), _ptrs(scales),
         _ptrs(global_scales), _ptrs(Hs), _i64s([s[0] for s in shapes]),
         _i64s([s[1] for s in shapes]), _ptrs(errs), _ptr(ws), nws, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# products with the solved weights, and tokens by expert and back
+# ---------------------------------------------------------------------------
+def _run_on(call, tensors, stream, *args):
+    """Calls the library with the device of the tensors current (they must
+    share one) and its current stream, or the given stream of that device."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"tensors on {dev} and {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG,
+                         f"stream of {stream.device}, tensors on {dev}")
+    fn = getattr(lib(), call)
+    if dev.index == torch.cuda.current_device():
+        code = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream.cuda_stream)
+    _check(call, code)
+
+
+def _weight(call, name, w, lead, d_out, d_in):
+    """(codes, scales, global_scale) of one matrix (lead = ()) or of lead[0]
+    experts' matrices one after another."""
+    if len(w) != 3:
+        raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"{name}: expected (codes, scales, "
+                                                      f"global_scale)")
+    codes, scales, sg = w
+    _need(call, codes, name + "codes", (*lead, d_out, d_in // 2), _U8)
+    _need(call, scales, name + "scales", (*lead, d_out, d_in // 16), _U8)
+    _need(call, sg, name + ("global_scales" if lead else "global_scale"), lead or (1,), _F32)
+    return codes.data_ptr(), scales.data_ptr(), sg.data_ptr()
+
+
+def _product(call, X, weights, Y, offsets, rows, stream):
+    """weights: [(name prefix, (codes, scales, global_scale))]."""
+    n_x, d_in = _matrix(call, X, "X", _IO_DTYPES)
+    n_rows, d_out = _matrix(call, Y, "Y", _IO_DTYPES)
+    tensors = [X, Y, *(t for _, w in weights for t in w)]
+    if d_in % 16:
+        raise Nvfp4Error(call, 2, f"X: {d_in} columns, not a multiple of 16")
+    if offsets is None:
+        if n_rows != n_x:
+            raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"X has {n_x} rows, Y {n_rows}")
+        lead, head = (), ()
+    else:
+        _need(call, offsets, "offsets", dtype=_I32, numel_min=1)
+        _need(call, offsets, "offsets", (offsets.numel(),))
+        tensors.append(offsets)
+        if rows is None:
+            if n_rows != n_x:
+                raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG,
+                                 f"X has {n_x} rows, Y {n_rows}, and rows is missing")
+        else:
+            _need(call, rows, "rows", (n_rows,), _I32)
+            tensors.append(rows)
+        lead = (offsets.numel() - 1,)
+        head = (None if rows is None else rows.data_ptr(), offsets.data_ptr(), lead[0], n_rows)
+    w = [p for name, t in weights for p in _weight(call, name, t, lead, d_out, d_in)]
+    _run_on(call, tensors, stream, X.data_ptr(), _dtype_code(X), n_x, *head, *w, d_out, d_in,
+            Y.data_ptr(), _dtype_code(Y))
+
+
+def nvfp4_gemv(X, codes, scales, global_scale, Y, stream=None):
+    """Y (n_tok x d_out) = X (n_tok x d_in) Q^T from the codes as solved; X and
+    Y each bf16 or fp32."""
+    _product("nvfp4_gemv", X, [("", (codes, scales, global_scale))], Y, None, None, stream)
+
+
+def nvfp4_gemv_swiglu(X, gate, up, Y, stream=None):
+    """Y = silu(X Qg^T) * (X Qu^T); gate, up: (codes, scales, global_scale)."""
+    _product("nvfp4_gemv_swiglu", X, [("gate ", gate), ("up ", up)], Y, None, None, stream)
+
+
+def nvfp4_gemv_experts(X, offsets, codes, scales, global_scales, Y, rows=None, stream=None):
+    """Y[r] = x_r Q_e^T for the rows offsets[e]..offsets[e+1]-1 of each expert e;
+    x_r is X[rows[r]], or X[r] without rows.  codes (experts, d_out, d_in/2),
+    scales (experts, d_out, d_in/16), global_scales (experts,).  Rows outside
+    every expert are left as they were."""
+    _product("nvfp4_gemv_experts", X, [("", (codes, scales, global_scales))], Y,
+             _need("nvfp4_gemv_experts", offsets, "offsets"), rows, stream)
+
+
+def nvfp4_gemv_swiglu_experts(X, offsets, gate, up, Y, rows=None, stream=None):
+    """nvfp4_gemv_swiglu by expert; gate, up: (codes, scales, global_scales)
+    stacked as for nvfp4_gemv_experts."""
+    _product("nvfp4_gemv_swiglu_experts", X, [("gate ", gate), ("up ", up)], Y,
+             _need("nvfp4_gemv_swiglu_experts", offsets, "offsets"), rows, stream)
+
+
+def on_stream(stream):
+    """Allocations and launches inside go to the given stream (None: as they
+    are)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def into(Y, X, d_out, stream, product, *args):
+    """product(*args, Y) with Y allocated (X's rows and dtype) unless given."""
+    with on_stream(stream):
+        if Y is None:
+            Y = torch.empty((X.shape[0], d_out), dtype=X.dtype, device=X.device)
+        product(*args, Y)
+    return Y
+
+
+def nvfp4_moe_sort(expert_ids, offsets, rows, position, stream=None):
+    """expert_ids (n_tok, top_k) int32 or int64 -> offsets (experts + 1,), rows
+    (n_tok * top_k,) and position (n_tok, top_k), all int32: the slots in a
+    stable order by expert; ids outside 0..experts-1 have no row (-1)."""
+    call = "nvfp4_moe_sort"
+    n_tok, top_k = _matrix(call, expert_ids, "expert_ids", (_I32, torch.int64))
+    _need(call, offsets, "offsets", dtype=_I32, numel_min=1)
+    _need(call, offsets, "offsets", (offsets.numel(),))
+    _need(call, rows, "rows", (n_tok * top_k,), _I32)
+    _need(call, position, "position", (n_tok, top_k), _I32)
+    _run_on(call, (expert_ids, offsets, rows, position), stream, expert_ids.data_ptr(),
+            expert_ids.element_size(), n_tok, top_k, offsets.numel() - 1, offsets.data_ptr(),
+            rows.data_ptr(), position.data_ptr())
+
+
+def nvfp4_moe_gather(X, position, Xs, stream=None):
+    """Xs[position[t, j]] = X[t]; rows that no slot names are left as they were."""
+    call = "nvfp4_moe_gather"
+    n_tok, d = _matrix(call, X, "X", _IO_DTYPES)
+    n_pos, top_k = _matrix(call, position, "position", _I32)
+    _need(call, position, "position", (n_tok, top_k))
+    _need(call, Xs, "Xs", (n_tok * top_k, d), X.dtype)
+    _run_on(call, (X, position, Xs), stream, X.data_ptr(), _dtype_code(X), position.data_ptr(),
+            n_tok, top_k, d, Xs.data_ptr())
+
+
+def nvfp4_moe_combine(Ys, position, Y, weights=None, stream=None):
+    """Y[t] = sum_j weights[t, j] Ys[position[t, j]] (weights fp32, or None for
+    1: the gradient of nvfp4_moe_gather)."""
+    call = "nvfp4_moe_combine"
+    n_tok, d = _matrix(call, Y, "Y", _IO_DTYPES)
+    _, top_k = _matrix(call, position, "position", _I32)
+    _need(call, position, "position", (n_tok, top_k))
+    _need(call, Ys, "Ys", (n_tok * top_k, d), _IO_DTYPES)
+    _opt_need(call, weights, "weights", shape=(n_tok, top_k), dtype=_F32)
+    tensors = (Ys, position, Y) if weights is None else (Ys, position, Y, weights)
+    _run_on(call, tensors, stream, Ys.data_ptr(), _dtype_code(Ys), position.data_ptr(),
+            None if weights is None else weights.data_ptr(), n_tok, top_k, d, Y.data_ptr(),
+            _dtype_code(Y))
+
+
+def nvfp4_moe_combine_backward(dY, Ys, position, weights, dYs, dweights, stream=None):
+    """Gradients of nvfp4_moe_combine: dYs[position[t, j]] = weights[t, j] dY[t],
+    dweights[t, j] = <dY[t], Ys[position[t, j]]>."""
+    call = "nvfp4_moe_combine_backward"
+    n_tok, d = _matrix(call, dY, "dY", _IO_DTYPES)
+    _, top_k = _matrix(call, position, "position", _I32)
+    _need(call, position, "position", (n_tok, top_k))
+    _need(call, Ys, "Ys", (n_tok * top_k, d), dY.dtype)
+    _need(call, dYs, "dYs", (n_tok * top_k, d), dY.dtype)
+    _need(call, weights, "weights", (n_tok, top_k), _F32)
+    _need(call, dweights, "dweights", (n_tok, top_k), _F32)
+    _run_on(call, (dY, Ys, position, weights, dYs, dweights), stream, dY.data_ptr(),
+            Ys.data_ptr(), _dtype_code(dY), position.data_ptr(), weights.data_ptr(), n_tok, top_k,
+            d, dYs.data_ptr(), dweights.data_ptr())

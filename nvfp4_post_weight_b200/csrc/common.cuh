@@ -67,7 +67,9 @@ enum Phase {
   kPhaseFactorGemm = 6,   // sub-phases of kPhasePrepare
   kPhasePanel = 7,
   kPhaseFactorI8 = 8,
-  kNumPhases = 9
+  kPhaseProduct = 9,
+  kPhaseRoute = 10,
+  kNumPhases = 11
 };
 // While profiling is on, adds algorithmic work (flops) to the open phase.
 void add_phase_work(double work);

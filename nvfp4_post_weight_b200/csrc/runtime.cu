@@ -85,7 +85,8 @@ void add_phase_work(double work) {
 // a push or pop costs a pointer test.
 static const char* const kPhaseRangeNames[] = {
     "nvfp4 hessian", "nvfp4 prepare", "nvfp4 replay", "nvfp4 update", "nvfp4 dequant",
-    "nvfp4 other",   "nvfp4 factor fp64 gemm", "nvfp4 panel", "nvfp4 factor int8 gemm"};
+    "nvfp4 other",   "nvfp4 factor fp64 gemm", "nvfp4 panel", "nvfp4 factor int8 gemm",
+    "nvfp4 product", "nvfp4 route"};
 
 ProfileScope::ProfileScope(int phase, cudaStream_t s) : slot(-1), prev_phase(t_phase), st(s) {
   t_phase = phase;

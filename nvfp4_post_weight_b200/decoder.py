@@ -83,6 +83,21 @@ class DecoderLayerSolver:
                 B.nvfp4_layer_error(W[n], self.codes[n], self.scales[n], self.s_g[n], H,
                                     self.layer_err[n], self.ws_err, stream)
 
+    def weight(self, name):
+        """(codes, scales, global scale) of a solved tensor."""
+        return self.codes[name], self.scales[name], self.s_g[name]
+
+    def linear(self, name, X, Y=None, stream=None):
+        """Y = X Q^T for a few tokens X from the solved codes of a tensor; Y of
+        X's dtype unless given."""
+        return B.into(Y, X, self.shapes[name][0], stream, B.nvfp4_gemv, X, *self.weight(name))
+
+    def gated(self, gate, up, X, Y=None, stream=None):
+        """Y = silu(X Qg^T) * (X Qu^T) from two solved tensors of one shape, the
+        input of the down projection."""
+        return B.into(Y, X, self.shapes[gate][0], stream, B.nvfp4_gemv_swiglu, X,
+                      self.weight(gate), self.weight(up))
+
     def step(self, W, X, stream=None, with_error=True):
         """W: {tensor name: device weights}, X: {x name: device tokens}."""
         for x, t in self.groups:
@@ -209,10 +224,18 @@ class MoELayerSolver:
         self.wshape = [s for _ in range(E) for s in ((inter, hidden), (inter, hidden),
                                                     (hidden, inter))]
         self.wfac = [2 * e + k for e in range(E) for k in (0, 0, 1)]
-        self.codes = [torch.empty((o, i // 2), dtype=torch.uint8, device=dev) for o, i in self.wshape]
-        self.scales = [torch.empty((o, i // 16), dtype=torch.uint8, device=dev)
-                       for o, i in self.wshape]
-        self.s_g = [torch.empty(1, dtype=torch.float32, device=dev) for _ in self.wshape]
+        # each projection's results lie expert after expert, as the products by
+        # expert read them; the lists hold every tensor's view
+        self.stacked = {}
+        for k, name in enumerate(("gate", "up", "down")):
+            o, i = self.wshape[k] if E else (0, 0)
+            self.stacked[name] = (torch.empty((E, o, i // 2), dtype=torch.uint8, device=dev),
+                                  torch.empty((E, o, i // 16), dtype=torch.uint8, device=dev),
+                                  torch.empty(E, dtype=torch.float32, device=dev))
+        kinds = [(e, self.stacked[name]) for e in range(E) for name in ("gate", "up", "down")]
+        self.codes = [c[e] for e, (c, _, _) in kinds]
+        self.scales = [s[e] for e, (_, s, _) in kinds]
+        self.s_g = [g[e:e + 1] for e, (_, _, g) in kinds]
         self.err = [torch.empty(1, dtype=torch.float64, device=dev) for _ in self.wshape]
         self.ws_quant = _flat(B.nvfp4_quantize_batched_workspace_size(self.wshape, self.params),
                               dev)
@@ -240,6 +263,48 @@ class MoELayerSolver:
             B.nvfp4_layer_error_batched(Ws, self.codes, self.scales, self.s_g,
                                         [self.H[f] for f in self.wfac], self.layer_err,
                                         self.ws_err, stream)
+
+    def sort(self, expert_ids, stream=None):
+        """(offsets, rows, position) of the routing slots by expert
+        (expert_ids: n_tok x top_k; an id outside the experts, as of a padded
+        token, has no row)."""
+        with B.on_stream(stream):
+            n, dev = expert_ids.numel(), expert_ids.device
+            offsets = torch.empty(self.E + 1, dtype=torch.int32, device=dev)
+            rows = torch.empty(n, dtype=torch.int32, device=dev)
+            position = torch.empty(expert_ids.shape, dtype=torch.int32, device=dev)
+            B.nvfp4_moe_sort(expert_ids, offsets, rows, position)
+        return offsets, rows, position
+
+    def tokens_by_expert(self, X, expert_ids, stream=None):
+        """[X_e]: every expert's routed tokens as one matrix each (views of one
+        array), the calibration input of its gate and up projections.  The
+        counts are read on the host, so this waits for the stream."""
+        with B.on_stream(stream):
+            offsets, _, position = self.sort(expert_ids)
+            Xs = torch.empty((expert_ids.numel(), X.shape[1]), dtype=X.dtype, device=X.device)
+            B.nvfp4_moe_gather(X, position, Xs)
+            ends = offsets.tolist()
+        return [Xs[a:b] for a, b in zip(ends, ends[1:])]
+
+    def forward(self, X, expert_ids, weights, Y=None, stream=None):
+        """The solved layer's answer for a few tokens: Y[t] = sum_j weights[t, j]
+        down_e(silu(gate_e x_t) * up_e x_t), e = expert_ids[t, j] (a slot whose
+        id is outside the experts adds nothing).  X n_tok x hidden, weights
+        n_tok x top_k fp32; Y of X's dtype unless given.  The intermediate is
+        rounded to X's dtype, the experts' answers are fp32."""
+        with B.on_stream(stream):
+            offsets, rows, position = self.sort(expert_ids)
+            n, dev = expert_ids.numel(), X.device
+            mid = torch.empty((n, self.inter), dtype=X.dtype, device=dev)
+            B.nvfp4_gemv_swiglu_experts(X, offsets, self.stacked["gate"], self.stacked["up"], mid,
+                                        rows)
+            out = torch.empty((n, self.hidden), dtype=torch.float32, device=dev)
+            B.nvfp4_gemv_experts(mid, offsets, *self.stacked["down"], out)
+            if Y is None:
+                Y = torch.empty_like(X)
+            B.nvfp4_moe_combine(out, position, Y, weights)
+        return Y
 
     def status(self, stream=None):
         """(prepare, quantize, layer-error, Hessian status): the first non-OK

@@ -55,6 +55,11 @@ class LayerSolver:
         B.nvfp4_layer_error(W, self.codes, self.scales, self.s_g, self.H, self.layer_err,
                             self.ws_err, stream)
 
+    def linear(self, X, Y=None, stream=None):
+        """Y = X Q^T for a few tokens X (n_tok x d_in, bf16 or fp32) from the
+        solved codes; Y of X's dtype unless given."""
+        return B.into(Y, X, self.d_out, stream, B.nvfp4_gemv, X, self.codes, self.scales, self.s_g)
+
     def step(self, W, X, stream=None, with_error=True):
         """One whole solve of the layer from its weights and calibration
         activations (both already on the device)."""

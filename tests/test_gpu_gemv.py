@@ -1,0 +1,337 @@
+"""Products of a few tokens with solved NVFP4 weights (nvfp4_gemv, its gated
+pair and both by expert) against fp64 products with the dequantised weights.
+
+Tolerances: the products x * e2m1 * e4m3 are exact, so what is left are the
+roundings of the fp32 sums.  Along any path from a product to the result there
+are at most K / 32 + 160 of them (a lane's share of the row, the steps inside
+one 128-column tile, the joins), each at most 2^-23 of the sum of absolute
+values S (twice the half step, for units that truncate); then one rounding of
+the output, half a step of its type relative to it.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from nvfp4_post_weight_b200 import binding as B
+from nvfp4_post_weight_b200 import synth
+from nvfp4_post_weight_b200.decoder import DecoderLayerSolver
+from nvfp4_post_weight_b200.layer import LayerSolver
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def weights(shape, seed, lo=60, hi=127):
+    g = torch.Generator().manual_seed(seed)
+    *lead, d_out, d_in = shape
+    codes = torch.randint(0, 256, (*lead, d_out, d_in // 2), generator=g, dtype=torch.uint8)
+    scales = torch.randint(lo, hi, (*lead, d_out, d_in // 16), generator=g, dtype=torch.uint8)
+    sg = torch.rand(lead[0] if lead else 1, generator=g) * 1e-3 + 1e-3
+    return codes.to(DEV), scales.to(DEV), sg.to(DEV)
+
+
+def dequantised(codes, scales, sg):
+    """fp64 weights of one matrix (device)."""
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device=DEV)
+    c = codes.long()
+    nib = torch.stack((c & 15, c >> 4), -1).reshape(c.shape[0], -1)
+    e4m3 = [(8 + (c & 7)) * 2.0 ** ((c >> 3) - 10) if c > 7 else c * 2.0 ** -9 for c in range(128)]
+    block = torch.tensor(e4m3, dtype=torch.float64, device=DEV)[(scales & 127).long()]
+    mag = grid[nib & 7]
+    return torch.where(nib > 7, -mag, mag) * block.repeat_interleave(16, 1) * sg.double()
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def sums(x, w):
+    """(product, tolerance of its fp32 sum) in fp64."""
+    x, q = x.double(), dequantised(*w)
+    K = q.shape[1]
+    return x @ q.T, (K / 32 + 160) * 2.0 ** -23 * (x.abs() @ q.abs().T)
+
+
+def gated(x, gate, up):
+    """(silu(g) u, tolerance): |silu'| <= 1.1, and eight roundings of expf, the
+    sum, the division and the product."""
+    (g, dg), (u, du) = sums(x, gate), sums(x, up)
+    s = g * torch.sigmoid(g)
+    return s * u, 1.1 * u.abs() * dg + s.abs() * du + 1.1 * dg * du + \
+        8 * 2.0 ** -23 * (s * u).abs() + 1e-36
+
+
+def close(y, ref, tol):
+    tol = tol + half_step(y.dtype) * (ref.abs() + tol) + 1e-38
+    bad = ~((y.double() - ref).abs() <= tol)
+    assert not bad.any(), ((y.double() - ref).abs() / tol).max().item()
+
+
+def acts(n, d, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((n, d), generator=g) * torch.exp(torch.randn(d, generator=g))
+    return x.to(dtype).to(DEV)
+
+
+SHAPES = [(1, 1, 16), (1, 16, 128), (3, 17, 144), (8, 33, 512), (9, 100, 1040), (5, 7, 4112),
+          (16, 64, 256), (17, 31, 272), (40, 130, 656), (1, 300, 8192), (2, 48, 28672),
+          (70, 257, 2064), (129, 24, 96)]
+
+
+@pytest.mark.parametrize("n_tok,d_out,d_in", SHAPES)
+@pytest.mark.parametrize("xt,yt", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+def test_gemv(n_tok, d_out, d_in, xt, yt):
+    w, x = weights((d_out, d_in), d_out + d_in), acts(n_tok, d_in, xt, n_tok)
+    y = torch.full((n_tok, d_out), 7.0, dtype=yt, device=DEV)
+    B.nvfp4_gemv(x, *w, y)
+    close(y, *sums(x, w))
+
+
+@pytest.mark.parametrize("n_tok,d_out,d_in", SHAPES)
+@pytest.mark.parametrize("xt,yt", [(BF16, BF16), (F32, F32)])
+def test_gemv_swiglu(n_tok, d_out, d_in, xt, yt):
+    gate, up = weights((d_out, d_in), 1 + d_in), weights((d_out, d_in), 2 + d_in)
+    x = acts(n_tok, d_in, xt, n_tok) * 0.1
+    y = torch.full((n_tok, d_out), 7.0, dtype=yt, device=DEV)
+    B.nvfp4_gemv_swiglu(x, gate, up, y)
+    close(y, *gated(x, gate, up))
+
+
+def test_every_code_and_scale():
+    """Each element code under each scale code (subnormal ones, 0 and the
+    largest among them), one nonzero token entry at a time: exact in fp32."""
+    d_in, codes = 16, np.arange(16)
+    nib = np.stack([np.roll(codes, r) for r in range(16)])            # 16 x 16
+    rows = np.repeat(nib, 128, axis=0)
+    packed = (rows[:, 0::2] | (rows[:, 1::2] << 4)).astype(np.uint8)
+    scales = np.tile(np.arange(128), 16).astype(np.uint8)[:, None]
+    w = (torch.from_numpy(packed).to(DEV), torch.from_numpy(scales).to(DEV),
+         torch.ones(1, device=DEV))
+    for xt in (BF16, F32):
+        x = torch.eye(16, dtype=xt, device=DEV)
+        y = torch.empty((16, 2048), dtype=F32, device=DEV)
+        B.nvfp4_gemv(x, *w, y)
+        assert torch.equal(y.double(), dequantised(*w).T)
+
+
+def test_fp32_tokens_keep_all_their_bits():
+    w = weights((50, 256), 3)
+    x = torch.zeros((4, 256), device=DEV)
+    x[0, 5], x[1, 17], x[2, 100], x[3, 255] = 1 + 2.0 ** -23, 16777215.0, -3.1415927, 1e-30
+    y = torch.empty((4, 50), device=DEV)
+    B.nvfp4_gemv(x, *w, y)
+    ref = x.double() @ dequantised(*w).T
+    # three pieces joined (at most 2^-23 each) and two products
+    assert ((y.double() - ref).abs() <= 8 * 2.0 ** -24 * ref.abs()).all()
+
+
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_extreme_tokens_and_scales(xt):
+    """Large and tiny tokens, and global scales near both ends of fp32."""
+    for mag, sg in ((1e30, 1e-3), (1e-30, 1e3), (1e3, 1e-36), (1e-3, 1e34)):
+        w = weights((40, 528), 11)
+        w[2].fill_(sg)
+        x = (acts(3, 528, F32, 5) * mag).to(xt)
+        y = torch.empty((3, 40), device=DEV)
+        B.nvfp4_gemv(x, *w, y)
+        ref, tol = sums(x, w)
+        assert ((y.double() - ref).abs() <= tol + 2.0 ** -23 * ref.abs() + 2.0 ** -148).all()
+
+
+@pytest.mark.parametrize("xt", [BF16, F32])
+@pytest.mark.parametrize("n_tok", [3, 20])
+def test_nonfinite_tokens_stay_in_their_row(xt, n_tok):
+    w, x = weights((70, 272), 21), acts(n_tok, 272, xt, 22)
+    x[1, 3], x[2, 200], x[2, 9] = float("nan"), float("inf"), 1.0
+    y = torch.empty((n_tok, 70), dtype=F32, device=DEV)
+    B.nvfp4_gemv(x, *w, y)
+    ref = (x.double()[:, None, :] * dequantised(*w)[None]).sum(-1)
+    assert torch.equal(torch.isnan(y), torch.isnan(ref))
+    inf = torch.isinf(ref)
+    assert inf.any() and torch.equal(y[inf].double(), ref[inf])
+    keep = [i for i in range(n_tok) if i not in (1, 2)]
+    close(y[keep], *sums(x[keep], w))
+
+
+def test_zero_blocks_and_empty_sizes():
+    codes, scales, sg = weights((20, 64), 4)
+    scales[3], codes[3] = 0, 0
+    x = acts(2, 64, BF16, 1)
+    y = torch.full((2, 20), 5.0, device=DEV)
+    B.nvfp4_gemv(x, codes, scales, sg, y)
+    assert (y[:, 3] == 0).all()
+    # no tokens, no outputs, no inputs (an empty sum: zeros, for the pair too)
+    B.nvfp4_gemv(x[:0], codes, scales, sg, y[:0])
+    B.nvfp4_gemv(x, codes[:0], scales[:0], sg, y[:, :0].contiguous())
+    e = (codes[:, :0].contiguous(), scales[:, :0].contiguous(), sg)
+    y.fill_(5.0)
+    B.nvfp4_gemv(x[:, :0].contiguous(), *e, y)
+    assert (y == 0).all()
+    y.fill_(5.0)
+    B.nvfp4_gemv_swiglu(x[:, :0].contiguous(), e, e, y)
+    assert (y == 0).all()
+
+
+@pytest.mark.parametrize("d_in", [64, 80, 1024, 1040])
+def test_unaligned_bases(d_in):
+    """Codes 8 bytes off a 16-byte boundary, scales at an odd byte, row slices."""
+    w = weights((40, d_in), 8)
+    x = acts(3, d_in, BF16, 2)
+    ref = sums(x, w)
+    codes = torch.empty(w[0].numel() + 8, dtype=torch.uint8, device=DEV)[8:].view(w[0].shape)
+    scales = torch.empty(w[1].numel() + 1, dtype=torch.uint8, device=DEV)[1:].view(w[1].shape)
+    codes.copy_(w[0])
+    scales.copy_(w[1])
+    buf = torch.empty(3 * 40 + 1, dtype=BF16, device=DEV)
+    y = buf[1:].view(3, 40)
+    B.nvfp4_gemv(x, codes, scales, w[2], y)
+    close(y, *ref)
+    y = torch.empty((3, 21), device=DEV)
+    B.nvfp4_gemv(x, codes[19:], scales[19:], w[2], y)
+    close(y, ref[0][:, 19:], ref[1][:, 19:])
+
+
+def test_the_same_call_twice_gives_the_same_bits():
+    w, x = weights((300, 2064), 31), acts(6, 2064, BF16, 3)
+    ys = [torch.empty((6, 300), device=DEV) for _ in range(2)]
+    for y in ys:
+        B.nvfp4_gemv(x, *w, y)
+    assert torch.equal(*ys)
+
+
+# ---- by expert ---------------------------------------------------------------
+def by_expert(fn, offsets, *ws):
+    """fn(row range, matrices of expert e) for every expert with rows."""
+    ends = offsets.tolist()
+    for e, (a, b) in enumerate(zip(ends, ends[1:])):
+        if b > a:
+            fn(slice(a, b), *[tuple((w[0][e], w[1][e], w[2][e])) for w in ws])
+
+
+COUNTS = [[1], [0, 3, 0, 0, 1, 0], [8, 0, 9, 1, 17, 0, 64], [0, 0, 0], [150, 1]]
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("d_out,d_in", [(40, 272), (136, 1024)])
+@pytest.mark.parametrize("xt,yt", [(BF16, F32), (F32, F32), (BF16, BF16)])
+def test_gemv_experts(counts, d_out, d_in, xt, yt):
+    E, n = len(counts), sum(counts)
+    extra = 5   # rows behind the last expert's stay as they were
+    w = weights((E, d_out, d_in), 5 + E)
+    x = acts(n + extra, d_in, xt, 9)
+    offsets = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
+    y = torch.full((n + extra, d_out), 7.0, dtype=yt, device=DEV)
+    B.nvfp4_gemv_experts(x, offsets, *w, y)
+    by_expert(lambda r, m: close(y[r], *sums(x[r], m)), offsets, w)
+    assert (y[n:] == 7).all()
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_gemv_swiglu_experts_with_rows(counts, xt):
+    E, n, d_out, d_in = len(counts), sum(counts), 72, 400
+    gate, up = weights((E, d_out, d_in), 50 + E), weights((E, d_out, d_in), 60 + E)
+    x = acts(11, d_in, xt, 9) * 0.1
+    rows = torch.randint(0, 11, (n + 3,), dtype=torch.int32, device=DEV)
+    offsets = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
+    y = torch.full((n + 3, d_out), 7.0, dtype=xt, device=DEV)
+    B.nvfp4_gemv_swiglu_experts(x, offsets, gate, up, y, rows)
+    xr = x[rows.long()]
+    by_expert(lambda r, g, u: close(y[r], *gated(xr[r], g, u)), offsets, gate, up)
+    assert (y[n:] == 7).all()
+
+
+def test_bad_offsets_and_rows_are_cut():
+    """Offsets beyond the rows are cut to them; a row index outside X reads as
+    zeros."""
+    w, x = weights((2, 24, 64), 1), acts(4, 64, BF16, 1)
+    offsets = torch.tensor([-3, 2, 9], dtype=torch.int32, device=DEV)
+    rows = torch.tensor([0, -1, 4, 3, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    y = torch.full((5, 24), 7.0, device=DEV)
+    B.nvfp4_gemv_experts(x, offsets, *w, y, rows)
+    for r, (e, src) in enumerate([(0, 0), (0, None), (1, None), (1, 3), (1, None)]):
+        if src is None:
+            assert (y[r] == 0).all()
+        else:
+            close(y[r:r + 1], *sums(x[src:src + 1], (w[0][e], w[1][e], w[2][e])))
+
+
+def test_descending_offsets_give_no_rows():
+    w, x = weights((2, 24, 64), 1), acts(4, 64, BF16, 1)
+    offsets = torch.tensor([3, 1, 2], dtype=torch.int32, device=DEV)
+    y = torch.full((4, 24), 7.0, device=DEV)
+    B.nvfp4_gemv_experts(x, offsets, *w, y)
+    assert (y[[0, 2, 3]] == 7).all()
+    close(y[1:2], *sums(x[1:2], (w[0][1], w[1][1], w[2][1])))
+
+
+def test_offsets_past_32_bits():
+    """The last of 1024 experts whose codes lie beyond 2^31 bytes."""
+    E, d_out, d_in = 1024, 1100, 4096
+    codes = torch.zeros((E, d_out, d_in // 2), dtype=torch.uint8, device=DEV)
+    scales = torch.zeros((E, d_out, d_in // 16), dtype=torch.uint8, device=DEV)
+    sg = torch.ones(E, device=DEV)
+    c, s, g = weights((d_out, d_in), 77)
+    codes[-1], scales[-1], sg[-1] = c, s, g[0]
+    x = acts(2, d_in, BF16, 4)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    offsets[1:-1], offsets[-1] = 1, 2
+    y = torch.full((2, d_out), 7.0, device=DEV)
+    B.nvfp4_gemv_experts(x, offsets, codes, scales, sg, y)
+    assert (y[0] == 0).all()
+    close(y[1:], *sums(x[1:], (c, s, g)))
+
+
+# ---- streams, graphs and the solvers -------------------------------------------
+def test_own_stream_and_graph_replay():
+    w, gate, up = weights((200, 512), 1), weights((200, 512), 2), weights((200, 512), 3)
+    x, y, z = acts(4, 512, BF16, 1), torch.empty((4, 200), device=DEV), \
+        torch.empty((4, 200), device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    B.nvfp4_gemv(x, *w, y, stream=side)
+    side.synchronize()
+    close(y, *sums(x, w))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.nvfp4_gemv(x, *w, y)
+        B.nvfp4_gemv_swiglu(x, gate, up, z)
+    for seed in (7, 8):
+        x.copy_(acts(4, 512, BF16, seed) * 0.1)
+        graph.replay()
+        torch.cuda.synchronize()
+        close(y, *sums(x, w))
+        close(z, *gated(x, gate, up))
+
+
+def test_a_solved_layer_answers():
+    W, X = synth.small_outlier(d_out=64, d_in=256, n_tok=512, seed=0)
+    s = LayerSolver(64, 256, DEV, out_dtype=F32)
+    s.step(W.to(DEV), X.to(DEV))
+    x = X[:5].to(DEV).to(BF16)
+    y = s.linear(x, torch.empty((5, 64), device=DEV))
+    ref = O.solve_layer(W.double().numpy(), X.double().numpy())
+    q = dequantised(s.codes, s.scales, s.s_g)
+    assert np.float32(s.s_g.item()) == ref["s_g"]
+    assert torch.equal(q.float(), s.Q)
+    close(y, *sums(x, (s.codes, s.scales, s.s_g)))
+    assert s.linear(x).dtype == BF16
+
+
+def test_a_solved_decoder_layer_answers():
+    groups = (("x", {"gate": (96, 64), "up": (96, 64)}), ("h", {"down": (64, 96)}))
+    s = DecoderLayerSolver(groups, DEV)
+    g = torch.Generator().manual_seed(1)
+    Ws = {n: (torch.randn(shape, generator=g) * 0.1).to(BF16).to(DEV)
+          for n, shape in s.shapes.items()}
+    s.step(Ws, {"x": acts(300, 64, BF16, 1), "h": acts(300, 96, BF16, 2)})
+    x = acts(3, 64, BF16, 3)
+    h = s.gated("gate", "up", x)
+    close(h, *gated(x, s.weight("gate"), s.weight("up")))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = s.linear("down", h, stream=side)
+    side.synchronize()
+    close(y, *sums(h, s.weight("down")))
