@@ -1,15 +1,37 @@
 // Products of a few tokens with NVFP4 weights as the solve leaves them:
 // Y = X Q^T, Q = e2m1(code) * e4m3(scale) * s_g, one matrix or one matrix per
 // expert over rows sorted by expert, and the gated pair silu(X Qg^T) * X Qu^T.
+//
+// The product e2m1 * e4m3 has at most six significant bits and is exact in
+// bf16, so a bf16 matrix instruction multiplies it with bf16 tokens exactly and
+// sums in fp32; fp32 tokens are cut into three bf16 pieces (exact: 8 bits
+// each), which take three instructions.  With few tokens the 9/16 byte per
+// weight bounds the product, and the decoding of the codes comes next: about
+// two integer instructions per weight.
+//
+// A warp takes 16 output columns (rows of Q; of both matrices for the pair)
+// over one slice of K, as the 16-row operand of mma.m16n8k16 with the tokens as
+// its 8 columns.  K is taken in chunks of 128: lane (g, t) holds the 32
+// weights 32 t .. 32 t + 31 of rows g and g + 8, one 16-byte load each, in
+// whatever order decoding leaves them, and the tokens in shared memory follow
+// that order (any order of K gives the same sum).  Eight warps with a tile
+// each share the tokens' slice; the slices of K are the CTAs of a cluster,
+// which add up their sums through distributed shared memory in a fixed order:
+// no workspace, no atomics, the same bits every time.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
 #include "common.cuh"
-#include "nvfp4_format.cuh"
 
 namespace nvfp4 {
 namespace {
 
-constexpr int kTok = 8;   // tokens per pass over a weight row
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 8;
+constexpr int kRowsCta = 16 * kWarps;
+constexpr int kChunk = 128;                   // K per step: 64 bytes of codes a row
+constexpr int kXSmem = 64 * 1024;             // tokens' share of shared memory
 
 struct ProductArgs {
   const void* X;
@@ -20,88 +42,399 @@ struct ProductArgs {
   const float* sg[2];
   void* Y;
   int64_t n_x, n_rows, d_out, d_in;
+  int n_experts;
+  int slice;            // chunks of K per CTA of the cluster
+  int stage;            // chunks of tokens in shared memory at a time
+  int y_bf16;
 };
 
-template <typename T>
-__device__ __forceinline__ float load1(const T* p) {
-  if constexpr (sizeof(T) == 2)
-    return __bfloat162float(*p);
-  else
-    return *p;
+// Eight codes (one word) as four bf16 pairs: elements (0,4), (1,5), (2,6),
+// (3,7).  A nibble s e e m times 0x1040 puts e e m at bits 6..8, the end of
+// the exponent and the top of the mantissa, and s at the sign: the bf16 (for
+// e e = 0 subnormal, with the right value) e2m1 * 2^-126.  Times the scale
+// e4m3 * 2^118 that is e2m1 * e4m3 * 2^-8, exact.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  __nv_bfloat162 r = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a),
+                             *reinterpret_cast<__nv_bfloat162*>(&b));
+  return *reinterpret_cast<uint32_t*>(&r);
+}
+__device__ __forceinline__ void decode8(uint32_t w, uint32_t scale, uint32_t* o) {
+  constexpr uint32_t kMask = 0x81C081C0u;
+  const uint32_t v = w >> 8;
+  o[0] = mul_bf16x2(((w & 0x000F000Fu) * 0x1040u) & kMask, scale);
+  o[1] = mul_bf16x2(((w & 0x00F000F0u) * 0x0104u) & kMask, scale);
+  o[2] = mul_bf16x2(((v & 0x000F000Fu) * 0x1040u) & kMask, scale);
+  o[3] = mul_bf16x2(((v & 0x00F000F0u) * 0x0104u) & kMask, scale);
 }
 
-// One warp per output column and matrix, one lane per block of 16 weights.
-template <typename TX, typename TY, bool kGlu>
-__global__ void __launch_bounds__(256) product_kernel(ProductArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t o = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (o >= a.d_out) return;
-  const int64_t e = blockIdx.y;
-  int64_t r0 = 0, r1 = a.n_rows;
-  if (a.offsets) {
-    r0 = min((int64_t)max(a.offsets[e], 0), a.n_rows);
-    r1 = min((int64_t)max(a.offsets[e + 1], 0), a.n_rows);
-  }
-  const int64_t nb = a.d_in / kBlock;
-  const int64_t wrow = (e * a.d_out + o) * nb;
-  for (int64_t t0 = r0; t0 < r1; t0 += kTok) {
-    float acc[kGlu ? 2 : 1][kTok] = {};
-    int64_t xr[kTok];
-    for (int t = 0; t < kTok; ++t) {
-      xr[t] = t0 + t < r1 ? (a.rows ? a.rows[t0 + t] : t0 + t) : -1;
-      if (xr[t] >= a.n_x) xr[t] = -1;
+// A scale code as a pair of bf16 e4m3 * 2^118: the code's seven bits at the
+// top of the fp32 mantissa are e4m3 * 2^-120 (subnormal codes included).
+__device__ __forceinline__ uint32_t scale_pair(uint32_t code) {
+  const float f = __uint_as_float((code & 0x7Fu) << 20) * 0x1p120f * 0x1p118f;
+  return __byte_perm(__float_as_uint(f), 0, 0x3232);
+}
+
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// One lane's codes and scales of one row in one chunk: 32 weights, 2 scales.
+struct Piece {
+  uint32_t c[4];
+  uint32_t s;
+};
+
+// block: the first of the lane's two blocks in the row; nb: blocks of the row;
+// blocks past the end are zero.  kWide: rows and bases allow 16-byte code and
+// 2-byte scale loads (then nb is even).
+template <bool kWide>
+__device__ __forceinline__ Piece load_piece(const uint8_t* codes, const uint8_t* scales, int block,
+                                            int nb) {
+  Piece p = {{0, 0, 0, 0}, 0};
+  if (kWide) {
+    if (block < nb) {
+      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(p.c[0]), "=r"(p.c[1]), "=r"(p.c[2]), "=r"(p.c[3])
+                   : "l"(codes + 8 * block));
+      p.s = __ldg(reinterpret_cast<const uint16_t*>(scales + block));
     }
-    for (int64_t b = lane; b < nb; b += 32) {
-      for (int m = 0; m < (kGlu ? 2 : 1); ++m) {
-        const uint2 c = reinterpret_cast<const uint2*>(a.codes[m])[wrow + b];
-        const uint64_t p = ((uint64_t)c.y << 32) | c.x;
-        const float sb = (float)e4m3_value(a.scales[m][wrow + b] & 0x7F);
-        for (int j = 0; j < kBlock; ++j) {
-          const float w = e2m1_value((uint32_t)(p >> (4 * j)) & 0xF) * sb;
-          for (int t = 0; t < kTok; ++t)
-            if (xr[t] >= 0)
-              acc[m][t] = fmaf(load1(static_cast<const TX*>(a.X) + xr[t] * a.d_in + b * kBlock + j),
-                               w, acc[m][t]);
+  } else {
+    if (block < nb) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(codes) + block);
+      p.c[0] = v.x;
+      p.c[1] = v.y;
+      p.s = __ldg(scales + block);
+    }
+    if (block + 1 < nb) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(codes) + block + 1);
+      p.c[2] = v.x;
+      p.c[3] = v.y;
+      p.s |= (uint32_t)__ldg(scales + block + 1) << 8;
+    }
+  }
+  return p;
+}
+
+// The tokens t0 .. t0 + n - 1 over chunks [c0, c1) in shared memory, in the
+// order that decode8 gives: per chunk and token 256 bytes, 16-byte unit
+// 4 i + t (XOR 4 for odd tokens: eight lanes then read all 32 banks) holds
+// elements 32 t + 8 i .. + 7 as the pairs (0,4), (1,5), (2,6), (3,7).  fp32
+// tokens take three planes.  Columns past d_in are zeros.
+template <typename TX>
+__device__ __forceinline__ void stage_tokens(const ProductArgs& a, int64_t t0, int n, int c0,
+                                             int c1, uint4* xs, int plane) {
+  const TX* X = static_cast<const TX*>(a.X);
+  const int units = (c1 - c0) * 16;
+  for (int i = threadIdx.x; i < n * units; i += blockDim.x) {
+    const int tok = i / units, u = i - tok * units;
+    const int64_t r = a.rows ? __ldg(a.rows + t0 + tok) : t0 + tok;
+    const int64_t k = (int64_t)c0 * kChunk + u * 8;
+    const int at = ((u >> 4) * n + tok) * 16 +
+                   ((((u & 3) << 2) | ((u >> 2) & 3)) ^ ((tok & 1) << 2));
+    const bool ok = k < a.d_in && r >= 0 && r < a.n_x;   // (d_in is a multiple of 8)
+    if constexpr (sizeof(TX) == 2) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (ok) v = __ldg(reinterpret_cast<const uint4*>(X + r * a.d_in + k));
+      xs[at] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                          __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+    } else {
+      float f[8] = {};
+      if (ok) {
+        const float4 lo = __ldg(reinterpret_cast<const float4*>(X + r * a.d_in + k));
+        const float4 hi = __ldg(reinterpret_cast<const float4*>(X + r * a.d_in + k) + 1);
+        f[0] = lo.x, f[1] = lo.y, f[2] = lo.z, f[3] = lo.w;
+        f[4] = hi.x, f[5] = hi.y, f[6] = hi.z, f[7] = hi.w;
+      }
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        // the upper halves are the next eight bits; an infinity leaves nothing
+        xs[p * plane + at] = make_uint4(
+            __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[4]), 0x7632),
+            __byte_perm(__float_as_uint(f[1]), __float_as_uint(f[5]), 0x7632),
+            __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[6]), 0x7632),
+            __byte_perm(__float_as_uint(f[3]), __float_as_uint(f[7]), 0x7632));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float top = __uint_as_float(__float_as_uint(f[j]) & 0xFFFF0000u);
+          f[j] = f[j] == top ? 0.f : f[j] - top;
         }
       }
     }
-    for (int t = 0; t < kTok; ++t) {
-      float v[2];
-      for (int m = 0; m < (kGlu ? 2 : 1); ++m) {
-        float s = acc[m][t];
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        v[m] = s * a.sg[m][e];
-      }
-      if (lane == 0 && t0 + t < r1) {
-        const float y = kGlu ? v[0] / (1.f + expf(-v[0])) * v[1] : v[0];
-        static_cast<TY*>(a.Y)[(t0 + t) * a.d_out + o] = (TY)y;
-      }
-    }
   }
 }
 
-template <typename TX, typename TY>
-void launch_typed(const ProductArgs& a, dim3 grid, bool glu, cudaStream_t st) {
-  if (glu)
-    product_kernel<TX, TY, true><<<grid, 256, 0, st>>>(a);
-  else
-    product_kernel<TX, TY, false><<<grid, 256, 0, st>>>(a);
+// The slot-th expert that has rows (offsets cut to 0..n_rows), and its rows;
+// -1 when there are fewer.  Warp-wide.
+__device__ __forceinline__ int find_expert(const ProductArgs& a, int slot, int64_t* r0,
+                                           int64_t* r1) {
+  const int lane = threadIdx.x & 31;
+  const int n = (int)a.n_rows;
+  for (int e0 = 0; e0 < a.n_experts; e0 += 128) {
+    int o[5], has = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      o[i] = min(max(__ldg(a.offsets + min(e0 + 4 * lane + i, a.n_experts)), 0), n);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) has += o[i + 1] > o[i];
+    int upto = has;   // inclusive scan over the lanes
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, upto > slot);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      int left = slot - (upto - has), e = 0, b = 0, c = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (o[i + 1] > o[i] && left-- == 0) e = e0 + 4 * lane + i, b = o[i], c = o[i + 1];
+      *r0 = __shfl_sync(0xffffffffu, b, src);
+      *r1 = __shfl_sync(0xffffffffu, c, src);
+      return __shfl_sync(0xffffffffu, e, src);
+    }
+    slot -= __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return -1;
 }
 
-nvfp4_status launch_product(const ProductArgs& a, nvfp4_dtype xt, nvfp4_dtype yt, int64_t n_experts,
+// NW matrices (2: the gated pair), NT * 8 tokens per pass, kWide as in
+// load_piece.  Grid: (cluster ranks fastest: slices of K) x tiles of 128
+// columns, and experts.
+template <typename TX, int NW, int NT, bool kWide>
+__global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const ProductArgs a) {
+  constexpr int kPlanes = sizeof(TX) == 2 ? 1 : 3;
+  constexpr int kDepth = NW == 1 ? 4 : 2;   // chunks loaded ahead
+  extern __shared__ uint4 smem[];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+
+  int64_t r0 = 0, r1 = a.n_rows;
+  int e = 0;
+  if (a.offsets) {
+    e = find_expert(a, blockIdx.y, &r0, &r1);
+    if (e < 0) return;   // (the whole cluster: it shares blockIdx.y)
+  }
+  const int64_t o0 = (int64_t)(blockIdx.x / S) * kRowsCta;
+  const int64_t row = o0 + warp * 16;
+  const int nb = (int)(a.d_in / kBlock);
+  const int n_chunks = (nb + 7) / 8;
+  const int c_begin = min(rank * a.slice, n_chunks), c_end = min(c_begin + a.slice, n_chunks);
+
+  // this lane's two rows of each matrix; rows past d_out read the last one
+  const uint8_t *codes[NW][2], *scales[NW][2];
+#pragma unroll
+  for (int m = 0; m < NW; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t r = (int64_t)e * a.d_out + min(row + g + 8 * h, a.d_out - 1);
+      codes[m][h] = a.codes[m] + r * nb * 8;
+      scales[m][h] = a.scales[m] + r * nb;
+    }
+
+  uint4* xs = smem;
+  const int max_tok = (int)min(r1 - r0, (int64_t)(8 * NT));
+  float* part = reinterpret_cast<float*>(smem + (size_t)kPlanes * a.stage * max_tok * 16);
+
+  for (int64_t t0 = r0; t0 < r1; t0 += 8 * NT) {
+    const int n = (int)min(r1 - t0, (int64_t)(8 * NT));
+    const int plane = a.stage * n * 16;
+    Piece q[kDepth][NW][2];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+      for (int m = 0; m < NW; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          q[d][m][h] = load_piece<kWide>(codes[m][h], scales[m][h],
+                                         c_begin + d < c_end ? (c_begin + d) * 8 + 2 * t : nb, nb);
+    float tot[NW][NT][4] = {};
+    for (int c0 = c_begin; c0 < c_end; c0 += a.stage) {
+      const int c1 = min(c0 + a.stage, c_end);
+      if (c0 > c_begin) __syncthreads();   // the previous tokens are used up
+      stage_tokens<TX>(a, t0, n, c0, c1, xs, plane);
+      __syncthreads();
+      for (int cb = c0; cb < c1; cb += kDepth) {   // (stage is a multiple of kDepth)
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) {
+          const int c = cb + d;
+          if (c >= c1) break;
+          float acc[NW][NT][4] = {};
+          uint32_t sc[NW][2][2];
+#pragma unroll
+          for (int m = 0; m < NW; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              sc[m][h][0] = scale_pair(q[d][m][h].s);
+              sc[m][h][1] = scale_pair(q[d][m][h].s >> 8);
+            }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t A[NW][2][4];
+#pragma unroll
+            for (int m = 0; m < NW; ++m) {
+              uint32_t p[2][4];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) decode8(q[d][m][h].c[w], sc[m][h][w >> 1], p[h]);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                A[m][j][0] = p[0][2 * j];
+                A[m][j][1] = p[1][2 * j];
+                A[m][j][2] = p[0][2 * j + 1];
+                A[m][j][3] = p[1][2 * j + 1];
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int tok = 8 * nt + g;
+#pragma unroll
+              for (int pl = 0; pl < kPlanes; ++pl) {
+                uint4 b = make_uint4(0, 0, 0, 0);
+                if (tok < n)
+                  b = xs[pl * plane + ((c - c0) * n + tok) * 16 + ((4 * w + t) ^ ((tok & 1) << 2))];
+#pragma unroll
+                for (int m = 0; m < NW; ++m) {
+                  mma(acc[m][nt], A[m][0], b.x, b.y);
+                  mma(acc[m][nt], A[m][1], b.z, b.w);
+                }
+              }
+            }
+          }
+          // The matrix unit does not round its sums to nearest; a chunk's sum
+          // goes to an fp32 total, so that its error does not grow with K.
+#pragma unroll
+          for (int m = 0; m < NW; ++m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) tot[m][nt][i] += acc[m][nt][i];
+          const int next = c + kDepth;
+#pragma unroll
+          for (int m = 0; m < NW; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              q[d][m][h] = load_piece<kWide>(codes[m][h], scales[m][h],
+                                             next < c_end ? next * 8 + 2 * t : nb, nb);
+        }
+      }
+    }
+    // sums of this slice: part[matrix][token][column]
+#pragma unroll
+    for (int m = 0; m < NW; ++m)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 8 * nt + 2 * t + (i & 1);
+          if (tok < n)
+            part[(m * max_tok + tok) * kRowsCta + warp * 16 + g + 8 * (i >> 1)] = tot[m][nt][i];
+        }
+    cluster.sync();
+    // each CTA joins and writes its share of the columns
+    const int share = kRowsCta / S;
+    for (int i = threadIdx.x; i < n * share; i += blockDim.x) {
+      const int tok = i / share, col = rank * share + i - tok * share;
+      if (o0 + col < a.d_out) {
+        float v[NW];
+#pragma unroll
+        for (int m = 0; m < NW; ++m) {
+          float s = 0.f;
+          for (int c = 0; c < S; ++c)
+            s += cluster.map_shared_rank(part, c)[(m * max_tok + tok) * kRowsCta + col];
+          v[m] = s * (0x1p8f * __ldg(a.sg[m] + e));
+        }
+        float y = v[0];
+        if constexpr (NW == 2) y = v[0] / (1.f + expf(-v[0])) * v[1];
+        const int64_t at = (t0 + tok) * a.d_out + o0 + col;
+        if (a.y_bf16)
+          static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(y);
+        else
+          static_cast<float*>(a.Y)[at] = y;
+      }
+    }
+    cluster.sync();   // the sums are read: part may be rewritten, the CTA may end
+  }
+}
+
+template <typename TX, int NW, int NT, bool kWide>
+nvfp4_status launch_kernel(const ProductArgs& a, dim3 grid, int S, size_t smem, cudaStream_t st) {
+  auto kernel = product_kernel<TX, NW, NT, kWide>;
+  if (smem > 48 * 1024)
+    NVFP4_CUDA_TRY(
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  NVFP4_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a));
+  return NVFP4_OK;
+}
+
+nvfp4_status launch_product(ProductArgs a, nvfp4_dtype xt, nvfp4_dtype yt, int64_t n_experts,
                             bool glu, cudaStream_t st) {
   if (a.n_rows == 0 || a.d_out == 0 || n_experts == 0) return NVFP4_OK;
   ProfileScope ps(kPhaseProduct, st);
-  const dim3 grid((unsigned)((a.d_out + 7) / 8), (unsigned)n_experts);
-  if (xt == NVFP4_BF16 && yt == NVFP4_BF16)
-    launch_typed<__nv_bfloat16, __nv_bfloat16>(a, grid, glu, st);
-  else if (xt == NVFP4_BF16)
-    launch_typed<__nv_bfloat16, float>(a, grid, glu, st);
-  else if (yt == NVFP4_BF16)
-    launch_typed<float, __nv_bfloat16>(a, grid, glu, st);
-  else
-    launch_typed<float, float>(a, grid, glu, st);
-  NVFP4_LAUNCH_CHECK();
+  a.n_experts = (int)n_experts;
+  a.y_bf16 = yt == NVFP4_BF16;
+  const int64_t tiles = (a.d_out + kRowsCta - 1) / kRowsCta;
+  const int64_t slots = n_experts < a.n_rows ? n_experts : a.n_rows;
+  const int n_chunks = (int)((a.d_in + kChunk - 1) / kChunk);
+  // slices of K: until the CTAs fill the GPU four times, each of four chunks at least
+  int S = 1;
+  while (S < 8 && tiles * slots * S < 4 * num_sms() && n_chunks >= 8 * S) S *= 2;
+  a.slice = (n_chunks + S - 1) / S;
+  // tokens per pass: the rows of one expert on average
+  const int64_t mean = (a.n_rows + slots - 1) / slots;
+  const int nt = mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
+  const int64_t tok = a.n_rows < 8 * nt ? a.n_rows : 8 * nt;
+  const int planes = xt == NVFP4_BF16 ? 1 : 3;
+  const int64_t per_chunk = planes * tok * 256;
+  int64_t stage = kXSmem / per_chunk / 4 * 4;
+  if (stage < 4) stage = 4;
+  if (stage > a.slice) stage = (a.slice + 3) / 4 * 4;
+  a.stage = (int)stage;
+  const size_t smem = stage * per_chunk + sizeof(float) * (glu ? 2 : 1) * tok * kRowsCta;
+  bool wide = a.d_in % 32 == 0;
+  for (int m = 0; m < (glu ? 2 : 1); ++m)
+    wide = wide && (reinterpret_cast<uintptr_t>(a.codes[m]) & 15) == 0 &&
+           (reinterpret_cast<uintptr_t>(a.scales[m]) & 1) == 0;
+  const dim3 grid((unsigned)(tiles * S), (unsigned)slots);
+  nvfp4_status s = NVFP4_ERR_INVALID_ARG;
+#define NVFP4_PRODUCT_W(TX, NW, NT)                                   \
+  s = wide ? launch_kernel<TX, NW, NT, true>(a, grid, S, smem, st)    \
+           : launch_kernel<TX, NW, NT, false>(a, grid, S, smem, st)
+#define NVFP4_PRODUCT(TX, NW)       \
+  if (nt == 1) {                    \
+    NVFP4_PRODUCT_W(TX, NW, 1);     \
+  } else if (nt == 2) {             \
+    NVFP4_PRODUCT_W(TX, NW, 2);     \
+  } else {                          \
+    NVFP4_PRODUCT_W(TX, NW, 4);     \
+  }
+  if (xt == NVFP4_BF16 && glu) {
+    NVFP4_PRODUCT(__nv_bfloat16, 2)
+  } else if (xt == NVFP4_BF16) {
+    NVFP4_PRODUCT(__nv_bfloat16, 1)
+  } else if (glu) {
+    NVFP4_PRODUCT(float, 2)
+  } else {
+    NVFP4_PRODUCT(float, 1)
+  }
+#undef NVFP4_PRODUCT
+#undef NVFP4_PRODUCT_W
+  if (s != NVFP4_OK) return s;
   count_launches(1);
   return NVFP4_OK;
 }
