@@ -473,15 +473,29 @@ nvfp4_status nvfp4_dequant_batched(int count, const uint8_t* const* codes,
  *           quantize call.
  * Y       : n_tok x d_out, bf16 or fp32 (y_dtype, its own choice), fully
  *           written; must not overlap X.  d_in == 0 gives zeros.
- * The products e2m1 * e4m3 are exact, their sums with X are fp32, and Y is
- * rounded once; bf16 and fp32 tokens are used at all their bits.  NaN and
- * infinite tokens behave as in the plain product and stay in their row.  Made
- * for few tokens, where the weights' bytes bound the product; any n_tok is
- * right.  No workspace, no status word.
+ * ws      : workspace of nvfp4_gemv_workspace_size(n_tok, d_in) bytes, 256-byte
+ *           aligned (0 for sizes that need none; NULL is then fine).  Its first
+ *           int is the status word (nvfp4_workspace_status): a timed-out wait
+ *           sets NVFP4_ERR_TIMEOUT, Y is then unspecified.
+ * The products are exact, their sums fp32, and Y is rounded once.  Sizes that
+ * need a workspace run on the block-scaled FP4 tensor cores where codes and
+ * scales are 16-byte aligned: there a token's entry is kept to 2^-22 of
+ * the largest of its block of 16 columns, or to 2^-39 of the token's largest
+ * where that is more (bf16 entries within 2^-14 of their block's largest are
+ * exact); elsewhere tokens are used at all their bits.  NaN and infinite
+ * tokens behave as in the plain product and stay in their row, and scale code
+ * 127 (a NaN, which the quantize call does not write) may give any value in
+ * its column.  Made for few tokens, where the weights' bytes bound the
+ * product; any n_tok is right.
  * d_out, n_tok <= 2^22, d_in <= 2^17 (NVFP4_ERR_SHAPE beyond). */
 nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const uint8_t* codes,
                         const uint8_t* scales, const float* global_scale, int64_t d_out,
-                        int64_t d_in, void* Y, nvfp4_dtype y_dtype, nvfp4_stream_t stream);
+                        int64_t d_in, void* Y, nvfp4_dtype y_dtype, void* ws,
+                        size_t ws_bytes, nvfp4_stream_t stream);
+
+/* Bytes of workspace of the products for n_rows rows of Y (n_tok, or the
+ * experts forms' n_rows) and d_in columns of X. */
+size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_in);
 
 /* The gated pair of a feed-forward layer in one pass:
  *   Y = silu(X Qg^T) * (X Qu^T),  silu(g) = g / (1 + exp(-g)),
@@ -492,7 +506,7 @@ nvfp4_status nvfp4_gemv_swiglu(const void* X, nvfp4_dtype x_dtype, int64_t n_tok
                                const float* gate_global_scale, const uint8_t* up_codes,
                                const uint8_t* up_scales, const float* up_global_scale,
                                int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype y_dtype,
-                               nvfp4_stream_t stream);
+                               void* ws, size_t ws_bytes, nvfp4_stream_t stream);
 
 /* Experts per call of the products by expert and of the routing calls. */
 #define NVFP4_MAX_EXPERTS 1024
@@ -515,13 +529,14 @@ nvfp4_status nvfp4_gemv_experts(const void* X, nvfp4_dtype x_dtype, int64_t n_x,
                                 const int32_t* rows, const int32_t* offsets, int64_t n_experts,
                                 int64_t n_rows, const uint8_t* codes, const uint8_t* scales,
                                 const float* global_scales, int64_t d_out, int64_t d_in, void* Y,
-                                nvfp4_dtype y_dtype, nvfp4_stream_t stream);
+                                nvfp4_dtype y_dtype, void* ws, size_t ws_bytes,
+                                nvfp4_stream_t stream);
 nvfp4_status nvfp4_gemv_swiglu_experts(
     const void* X, nvfp4_dtype x_dtype, int64_t n_x, const int32_t* rows, const int32_t* offsets,
     int64_t n_experts, int64_t n_rows, const uint8_t* gate_codes, const uint8_t* gate_scales,
     const float* gate_global_scales, const uint8_t* up_codes, const uint8_t* up_scales,
     const float* up_global_scales, int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype y_dtype,
-    nvfp4_stream_t stream);
+    void* ws, size_t ws_bytes, nvfp4_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Tokens by expert and back                                                 */

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -117,12 +118,15 @@ def _load(path):
                                vp], i32),
         "nvfp4_layer_error_workspace_size": ([i64, i64], sz),
         "nvfp4_layer_error": ([vp, i32, vp, vp, vp, vp, i64, i64, vp, vp, sz, vp], i32),
-        "nvfp4_gemv": ([vp, i32, i64, vp, vp, vp, i64, i64, vp, i32, vp], i32),
-        "nvfp4_gemv_swiglu": ([vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp], i32),
-        "nvfp4_gemv_experts": ([vp, i32, i64, vp, vp, i64, i64, vp, vp, vp, i64, i64, vp, i32, vp],
-                               i32),
+        "nvfp4_gemv_workspace_size": ([i64, i64], sz),
+        "nvfp4_gemv": ([vp, i32, i64, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp], i32),
+        "nvfp4_gemv_swiglu": ([vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp],
+                              i32),
+        "nvfp4_gemv_experts": (
+            [vp, i32, i64, vp, vp, i64, i64, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp], i32),
         "nvfp4_gemv_swiglu_experts": (
-            [vp, i32, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp], i32),
+            [vp, i32, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp],
+            i32),
         "nvfp4_moe_sort": ([vp, i32, i64, i64, i64, vp, vp, vp, vp], i32),
         "nvfp4_moe_gather": ([vp, i32, vp, i64, i64, i64, vp, vp], i32),
         "nvfp4_moe_combine": ([vp, i32, vp, vp, i64, i64, i64, vp, i32, vp], i32),
@@ -626,18 +630,26 @@ def nvfp4_layer_error_batched(Ws, codes, scales, global_scales, Hs, errs, ws, st
 # ---------------------------------------------------------------------------
 # products with the solved weights, and tokens by expert and back
 # ---------------------------------------------------------------------------
-def _run_on(call, tensors, stream, *args):
-    """Calls the library with the device of the tensors current (they must
-    share one) and its current stream, or the given stream of that device."""
+def _stream_of(call, tensors, stream):
+    """The given stream, or the current one, of the device that the tensors
+    must share."""
     dev = tensors[0].device
     for t in tensors:
         if t.device != dev:
             raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"tensors on {dev} and {t.device}")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
+        return torch.cuda.current_stream(dev)
+    if stream.device != dev:
         raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG,
                          f"stream of {stream.device}, tensors on {dev}")
+    return stream
+
+
+def _run_on(call, tensors, stream, *args):
+    """Calls the library on a stream of the tensors' device, with that device
+    current."""
+    stream = _stream_of(call, tensors, stream)
+    dev = tensors[0].device
     fn = getattr(lib(), call)
     if dev.index == torch.cuda.current_device():
         code = fn(*args, stream.cuda_stream)
@@ -660,7 +672,13 @@ def _weight(call, name, w, lead, d_out, d_in):
     return codes.data_ptr(), scales.data_ptr(), sg.data_ptr()
 
 
-def _product(call, X, weights, Y, offsets, rows, stream):
+@functools.lru_cache(maxsize=1024)
+def nvfp4_gemv_workspace_size(n_rows, d_in) -> int:
+    """Workspace bytes of a product with n_rows rows of Y and d_in columns of X."""
+    return int(lib().nvfp4_gemv_workspace_size(int(n_rows), int(d_in)))
+
+
+def _product(call, X, weights, Y, offsets, rows, ws, stream):
     """weights: [(name prefix, (codes, scales, global_scale))]."""
     n_x, d_in = _matrix(call, X, "X", _IO_DTYPES)
     n_rows, d_out = _matrix(call, Y, "Y", _IO_DTYPES)
@@ -685,35 +703,47 @@ def _product(call, X, weights, Y, offsets, rows, stream):
         lead = (offsets.numel() - 1,)
         head = (None if rows is None else rows.data_ptr(), offsets.data_ptr(), lead[0], n_rows)
     w = [p for name, t in weights for p in _weight(call, name, t, lead, d_out, d_in)]
+    nws = nvfp4_gemv_workspace_size(n_rows, d_in)
+    if ws is not None:
+        _ws_bytes(call, ws, nws)
+        tensors.append(ws)
+    elif nws:   # from torch's pool of the stream it is used on
+        with on_stream(_stream_of(call, tensors, stream)):
+            ws = workspace(nws, X.device)
     _run_on(call, tensors, stream, X.data_ptr(), _dtype_code(X), n_x, *head, *w, d_out, d_in,
-            Y.data_ptr(), _dtype_code(Y))
+            Y.data_ptr(), _dtype_code(Y), None if ws is None else ws.data_ptr(),
+            0 if ws is None else ws.numel())
 
 
-def nvfp4_gemv(X, codes, scales, global_scale, Y, stream=None):
+def nvfp4_gemv(X, codes, scales, global_scale, Y, ws=None, stream=None):
     """Y (n_tok x d_out) = X (n_tok x d_in) Q^T from the codes as solved; X and
-    Y each bf16 or fp32."""
-    _product("nvfp4_gemv", X, [("", (codes, scales, global_scale))], Y, None, None, stream)
+    Y each bf16 or fp32.  ws: nvfp4_gemv_workspace_size(n_tok, d_in) bytes
+    (here and below; torch's allocator provides them otherwise)."""
+    _product("nvfp4_gemv", X, [("", (codes, scales, global_scale))], Y, None, None, ws, stream)
 
 
-def nvfp4_gemv_swiglu(X, gate, up, Y, stream=None):
+def nvfp4_gemv_swiglu(X, gate, up, Y, ws=None, stream=None):
     """Y = silu(X Qg^T) * (X Qu^T); gate, up: (codes, scales, global_scale)."""
-    _product("nvfp4_gemv_swiglu", X, [("gate ", gate), ("up ", up)], Y, None, None, stream)
+    _product("nvfp4_gemv_swiglu", X, [("gate ", gate), ("up ", up)], Y, None, None, ws, stream)
 
 
-def nvfp4_gemv_experts(X, offsets, codes, scales, global_scales, Y, rows=None, stream=None):
+def nvfp4_gemv_experts(X, offsets, codes, scales, global_scales, Y, rows=None, ws=None,
+                       stream=None):
     """Y[r] = x_r Q_e^T for the rows offsets[e]..offsets[e+1]-1 of each expert e;
     x_r is X[rows[r]], or X[r] without rows.  codes (experts, d_out, d_in/2),
     scales (experts, d_out, d_in/16), global_scales (experts,).  Rows outside
     every expert are left as they were."""
-    _product("nvfp4_gemv_experts", X, [("", (codes, scales, global_scales))], Y,
-             _need("nvfp4_gemv_experts", offsets, "offsets"), rows, stream)
+    call = "nvfp4_gemv_experts"
+    _product(call, X, [("", (codes, scales, global_scales))], Y, _need(call, offsets, "offsets"),
+             rows, ws, stream)
 
 
-def nvfp4_gemv_swiglu_experts(X, offsets, gate, up, Y, rows=None, stream=None):
+def nvfp4_gemv_swiglu_experts(X, offsets, gate, up, Y, rows=None, ws=None, stream=None):
     """nvfp4_gemv_swiglu by expert; gate, up: (codes, scales, global_scales)
     stacked as for nvfp4_gemv_experts."""
-    _product("nvfp4_gemv_swiglu_experts", X, [("gate ", gate), ("up ", up)], Y,
-             _need("nvfp4_gemv_swiglu_experts", offsets, "offsets"), rows, stream)
+    call = "nvfp4_gemv_swiglu_experts"
+    _product(call, X, [("gate ", gate), ("up ", up)], Y, _need(call, offsets, "offsets"), rows, ws,
+             stream)
 
 
 def on_stream(stream):

@@ -19,9 +19,8 @@
 // which add up their sums through distributed shared memory in a fixed order:
 // no workspace, no atomics, the same bits every time.
 #include <cooperative_groups.h>
-#include <cuda_bf16.h>
 
-#include "common.cuh"
+#include "gemv.cuh"
 
 namespace nvfp4 {
 namespace {
@@ -33,19 +32,10 @@ constexpr int kRowsCta = 16 * kWarps;
 constexpr int kChunk = 128;                   // K per step: 64 bytes of codes a row
 constexpr int kXSmem = 64 * 1024;             // tokens' share of shared memory
 
-struct ProductArgs {
-  const void* X;
-  const int* rows;      // X row of each sorted row, or null
-  const int* offsets;   // n_experts + 1 row offsets, or null (one matrix)
-  const uint8_t* codes[2];
-  const uint8_t* scales[2];
-  const float* sg[2];
-  void* Y;
-  int64_t n_x, n_rows, d_out, d_in;
-  int n_experts;
+struct Args {
+  Product p;
   int slice;            // chunks of K per CTA of the cluster
   int stage;            // chunks of tokens in shared memory at a time
-  int y_bf16;
 };
 
 // Eight codes (one word) as four bf16 pairs: elements (0,4), (1,5), (2,6),
@@ -125,7 +115,7 @@ __device__ __forceinline__ Piece load_piece(const uint8_t* codes, const uint8_t*
 // elements 32 t + 8 i .. + 7 as the pairs (0,4), (1,5), (2,6), (3,7).  fp32
 // tokens take three planes.  Columns past d_in are zeros.
 template <typename TX>
-__device__ __forceinline__ void stage_tokens(const ProductArgs& a, int64_t t0, int n, int c0,
+__device__ __forceinline__ void stage_tokens(const Product& a, int64_t t0, int n, int c0,
                                              int c1, uint4* xs, int plane) {
   const TX* X = static_cast<const TX*>(a.X);
   const int units = (c1 - c0) * 16;
@@ -167,45 +157,11 @@ __device__ __forceinline__ void stage_tokens(const ProductArgs& a, int64_t t0, i
   }
 }
 
-// The slot-th expert that has rows (offsets cut to 0..n_rows), and its rows;
-// -1 when there are fewer.  Warp-wide.
-__device__ __forceinline__ int find_expert(const ProductArgs& a, int slot, int64_t* r0,
-                                           int64_t* r1) {
-  const int lane = threadIdx.x & 31;
-  const int n = (int)a.n_rows;
-  for (int e0 = 0; e0 < a.n_experts; e0 += 128) {
-    int o[5], has = 0;
-#pragma unroll
-    for (int i = 0; i < 5; ++i)
-      o[i] = min(max(__ldg(a.offsets + min(e0 + 4 * lane + i, a.n_experts)), 0), n);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) has += o[i + 1] > o[i];
-    int upto = has;   // inclusive scan over the lanes
-    for (int d = 1; d < 32; d <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += v;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, upto > slot);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      int left = slot - (upto - has), e = 0, b = 0, c = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (o[i + 1] > o[i] && left-- == 0) e = e0 + 4 * lane + i, b = o[i], c = o[i + 1];
-      *r0 = __shfl_sync(0xffffffffu, b, src);
-      *r1 = __shfl_sync(0xffffffffu, c, src);
-      return __shfl_sync(0xffffffffu, e, src);
-    }
-    slot -= __shfl_sync(0xffffffffu, upto, 31);
-  }
-  return -1;
-}
-
 // NW matrices (2: the gated pair), NT * 8 tokens per pass, kWide as in
 // load_piece.  Grid: (cluster ranks fastest: slices of K) x tiles of 128
 // columns, and experts.
 template <typename TX, int NW, int NT, bool kWide>
-__global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const ProductArgs a) {
+__global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const Args args) {
   constexpr int kPlanes = sizeof(TX) == 2 ? 1 : 3;
   constexpr int kDepth = NW == 1 ? 4 : 2;   // chunks loaded ahead
   extern __shared__ uint4 smem[];
@@ -213,17 +169,16 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
 
-  int64_t r0 = 0, r1 = a.n_rows;
-  int e = 0;
-  if (a.offsets) {
-    e = find_expert(a, blockIdx.y, &r0, &r1);
-    if (e < 0) return;   // (the whole cluster: it shares blockIdx.y)
-  }
+  const Product& a = args.p;
+  int e, first, count;
+  if (!find_pass(a, (int)a.n_rows, blockIdx.y, &e, &first, &count))
+    return;   // (the whole cluster: it shares blockIdx.y)
+  const int64_t r0 = first, r1 = first + count;
   const int64_t o0 = (int64_t)(blockIdx.x / S) * kRowsCta;
   const int64_t row = o0 + warp * 16;
-  const int nb = (int)(a.d_in / kBlock);
+  const int nb = a.nb;
   const int n_chunks = (nb + 7) / 8;
-  const int c_begin = min(rank * a.slice, n_chunks), c_end = min(c_begin + a.slice, n_chunks);
+  const int c_begin = min(rank * args.slice, n_chunks), c_end = min(c_begin + args.slice, n_chunks);
 
   // this lane's two rows of each matrix; rows past d_out read the last one
   const uint8_t *codes[NW][2], *scales[NW][2];
@@ -238,11 +193,11 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
 
   uint4* xs = smem;
   const int max_tok = (int)min(r1 - r0, (int64_t)(8 * NT));
-  float* part = reinterpret_cast<float*>(smem + (size_t)kPlanes * a.stage * max_tok * 16);
+  float* part = reinterpret_cast<float*>(smem + (size_t)kPlanes * args.stage * max_tok * 16);
 
   for (int64_t t0 = r0; t0 < r1; t0 += 8 * NT) {
     const int n = (int)min(r1 - t0, (int64_t)(8 * NT));
-    const int plane = a.stage * n * 16;
+    const int plane = args.stage * n * 16;
     Piece q[kDepth][NW][2];
 #pragma unroll
     for (int d = 0; d < kDepth; ++d)
@@ -253,8 +208,8 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
           q[d][m][h] = load_piece<kWide>(codes[m][h], scales[m][h],
                                          c_begin + d < c_end ? (c_begin + d) * 8 + 2 * t : nb, nb);
     float tot[NW][NT][4] = {};
-    for (int c0 = c_begin; c0 < c_end; c0 += a.stage) {
-      const int c1 = min(c0 + a.stage, c_end);
+    for (int c0 = c_begin; c0 < c_end; c0 += args.stage) {
+      const int c1 = min(c0 + args.stage, c_end);
       if (c0 > c_begin) __syncthreads();   // the previous tokens are used up
       stage_tokens<TX>(a, t0, n, c0, c1, xs, plane);
       __syncthreads();
@@ -347,13 +302,7 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
             s += cluster.map_shared_rank(part, c)[(m * max_tok + tok) * kRowsCta + col];
           v[m] = s * (0x1p8f * __ldg(a.sg[m] + e));
         }
-        float y = v[0];
-        if constexpr (NW == 2) y = v[0] / (1.f + expf(-v[0])) * v[1];
-        const int64_t at = (t0 + tok) * a.d_out + o0 + col;
-        if (a.y_bf16)
-          static_cast<__nv_bfloat16*>(a.Y)[at] = __float2bfloat16_rn(y);
-        else
-          static_cast<float*>(a.Y)[at] = y;
+        write_product<NW>(a, v, t0 + tok, o0 + col);
       }
     }
     cluster.sync();   // the sums are read: part may be rewritten, the CTA may end
@@ -361,7 +310,7 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
 }
 
 template <typename TX, int NW, int NT, bool kWide>
-nvfp4_status launch_kernel(const ProductArgs& a, dim3 grid, int S, size_t smem, cudaStream_t st) {
+nvfp4_status launch_kernel(const Args& a, dim3 grid, int S, size_t smem, cudaStream_t st) {
   auto kernel = product_kernel<TX, NW, NT, kWide>;
   if (smem > 48 * 1024)
     NVFP4_CUDA_TRY(
@@ -382,38 +331,36 @@ nvfp4_status launch_kernel(const ProductArgs& a, dim3 grid, int S, size_t smem, 
   return NVFP4_OK;
 }
 
-nvfp4_status launch_product(ProductArgs a, nvfp4_dtype xt, nvfp4_dtype yt, int64_t n_experts,
-                            bool glu, cudaStream_t st) {
-  if (a.n_rows == 0 || a.d_out == 0 || n_experts == 0) return NVFP4_OK;
-  ProfileScope ps(kPhaseProduct, st);
-  a.n_experts = (int)n_experts;
-  a.y_bf16 = yt == NVFP4_BF16;
-  const int64_t tiles = (a.d_out + kRowsCta - 1) / kRowsCta;
-  const int64_t slots = n_experts < a.n_rows ? n_experts : a.n_rows;
-  const int n_chunks = (int)((a.d_in + kChunk - 1) / kChunk);
+nvfp4_status launch_general(const Product& p, cudaStream_t st) {
+  Args a{};
+  a.p = p;
+  const bool glu = p.n_w == 2;
+  const int64_t tiles = (p.d_out + kRowsCta - 1) / kRowsCta;
+  const int64_t slots = !p.offsets ? 1 : p.n_experts < p.n_rows ? p.n_experts : p.n_rows;
+  const int n_chunks = (int)((p.d_in + kChunk - 1) / kChunk);
   // slices of K: until the CTAs fill the GPU four times, each of four chunks at least
   int S = 1;
   while (S < 8 && tiles * slots * S < 4 * num_sms() && n_chunks >= 8 * S) S *= 2;
   a.slice = (n_chunks + S - 1) / S;
   // tokens per pass: the rows of one expert on average
-  const int64_t mean = (a.n_rows + slots - 1) / slots;
+  const int64_t mean = (p.n_rows + slots - 1) / slots;
   const int nt = mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
-  const int64_t tok = a.n_rows < 8 * nt ? a.n_rows : 8 * nt;
-  const int planes = xt == NVFP4_BF16 ? 1 : 3;
+  const int64_t tok = p.n_rows < 8 * nt ? p.n_rows : 8 * nt;
+  const int planes = p.x_bf16 ? 1 : 3;
   const int64_t per_chunk = planes * tok * 256;
   int64_t stage = kXSmem / per_chunk / 4 * 4;
   if (stage < 4) stage = 4;
   if (stage > a.slice) stage = (a.slice + 3) / 4 * 4;
   a.stage = (int)stage;
-  const size_t smem = stage * per_chunk + sizeof(float) * (glu ? 2 : 1) * tok * kRowsCta;
-  bool wide = a.d_in % 32 == 0;
-  for (int m = 0; m < (glu ? 2 : 1); ++m)
-    wide = wide && (reinterpret_cast<uintptr_t>(a.codes[m]) & 15) == 0 &&
-           (reinterpret_cast<uintptr_t>(a.scales[m]) & 1) == 0;
+  const size_t smem = stage * per_chunk + sizeof(float) * p.n_w * tok * kRowsCta;
+  bool wide = p.d_in % 32 == 0;
+  for (int m = 0; m < p.n_w; ++m)
+    wide = wide && (reinterpret_cast<uintptr_t>(p.codes[m]) & 15) == 0 &&
+           (reinterpret_cast<uintptr_t>(p.scales[m]) & 1) == 0;
   const dim3 grid((unsigned)(tiles * S), (unsigned)slots);
   nvfp4_status s = NVFP4_ERR_INVALID_ARG;
-#define NVFP4_PRODUCT_W(TX, NW, NT)                                   \
-  s = wide ? launch_kernel<TX, NW, NT, true>(a, grid, S, smem, st)    \
+#define NVFP4_PRODUCT_W(TX, NW, NT)                                \
+  s = wide ? launch_kernel<TX, NW, NT, true>(a, grid, S, smem, st) \
            : launch_kernel<TX, NW, NT, false>(a, grid, S, smem, st)
 #define NVFP4_PRODUCT(TX, NW)       \
   if (nt == 1) {                    \
@@ -423,9 +370,9 @@ nvfp4_status launch_product(ProductArgs a, nvfp4_dtype xt, nvfp4_dtype yt, int64
   } else {                          \
     NVFP4_PRODUCT_W(TX, NW, 4);     \
   }
-  if (xt == NVFP4_BF16 && glu) {
+  if (p.x_bf16 && glu) {
     NVFP4_PRODUCT(__nv_bfloat16, 2)
-  } else if (xt == NVFP4_BF16) {
+  } else if (p.x_bf16) {
     NVFP4_PRODUCT(__nv_bfloat16, 1)
   } else if (glu) {
     NVFP4_PRODUCT(float, 2)
@@ -434,9 +381,8 @@ nvfp4_status launch_product(ProductArgs a, nvfp4_dtype xt, nvfp4_dtype yt, int64
   }
 #undef NVFP4_PRODUCT
 #undef NVFP4_PRODUCT_W
-  if (s != NVFP4_OK) return s;
-  count_launches(1);
-  return NVFP4_OK;
+  if (s == NVFP4_OK) count_launches(1);
+  return s;
 }
 
 constexpr int64_t kMaxDim = 1 << 17, kMaxRows = 1 << 22;
@@ -454,37 +400,48 @@ struct Matrix {
 // matrix, n_x == n_rows.
 nvfp4_status product(const void* X, nvfp4_dtype xt, int64_t n_x, const int* rows,
                      const int* offsets, int64_t n_experts, int64_t n_rows, const Matrix* w,
-                     int n_w, int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype yt,
-                     nvfp4_stream_t stream) {
+                     int n_w, int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype yt, void* ws,
+                     size_t ws_bytes, nvfp4_stream_t stream) {
   if (n_x < 0 || n_rows < 0 || n_experts < 0 || d_out < 0 || d_in < 0) return NVFP4_ERR_INVALID_ARG;
   if (!is_io(xt) || !is_io(yt)) return NVFP4_ERR_INVALID_ARG;
   if (d_in % kBlock || d_in > kMaxDim || d_out > kMaxRows || n_rows > kMaxRows || n_x > kMaxRows ||
       n_experts > NVFP4_MAX_EXPERTS)
     return NVFP4_ERR_SHAPE;
-  ProductArgs a{};
+  const bool any = n_rows > 0 && d_out > 0 && n_experts > 0;
+  Product p{};
   for (int m = 0; m < n_w; ++m) {
-    if (n_rows > 0 && d_out > 0 && n_experts > 0 &&
-        (!w[m].sg || (d_in > 0 && (!w[m].codes || !w[m].scales))))
+    if (any && (!w[m].sg || (d_in > 0 && (!w[m].codes || !w[m].scales))))
       return NVFP4_ERR_INVALID_ARG;
     if (!is_aligned(w[m].codes, 8) || !is_aligned(w[m].sg, 4)) return NVFP4_ERR_INVALID_ARG;
-    a.codes[m] = w[m].codes;
-    a.scales[m] = w[m].scales;
-    a.sg[m] = w[m].sg;
+    p.codes[m] = w[m].codes;
+    p.scales[m] = w[m].scales;
+    p.sg[m] = w[m].sg;
   }
-  if (n_rows > 0 && d_out > 0 && n_experts > 0 && (!Y || (n_x > 0 && d_in > 0 && !X)))
-    return NVFP4_ERR_INVALID_ARG;
+  if (any && (!Y || (n_x > 0 && d_in > 0 && !X))) return NVFP4_ERR_INVALID_ARG;
   if (!is_aligned(X, 16) || !is_aligned(Y, yt == NVFP4_BF16 ? 2 : 4) || !is_aligned(rows, 4) ||
       !is_aligned(offsets, 4))
     return NVFP4_ERR_INVALID_ARG;
-  a.X = X;
-  a.rows = rows;
-  a.offsets = offsets;
-  a.Y = Y;
-  a.n_x = n_x;
-  a.n_rows = n_rows;
-  a.d_out = d_out;
-  a.d_in = d_in;
-  return launch_product(a, xt, yt, n_experts, n_w == 2, as_cuda(stream));
+  const size_t need = any && product_fp4_shape(n_rows, d_in) ? product_fp4_ws_bytes(n_rows, d_in) : 0;
+  if (need && (!ws || !is_aligned(ws, 256) || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
+  if (!any) return NVFP4_OK;
+  p.X = X;
+  p.rows = rows;
+  p.offsets = offsets;
+  p.Y = Y;
+  p.n_x = n_x;
+  p.n_rows = n_rows;
+  p.n_experts = n_experts;
+  p.d_out = d_out;
+  p.d_in = d_in;
+  p.nb = (int)(d_in / kBlock);
+  p.n_w = n_w;
+  p.x_bf16 = xt == NVFP4_BF16;
+  p.y_bf16 = yt == NVFP4_BF16;
+  cudaStream_t st = as_cuda(stream);
+  ProfileScope ps(kPhaseProduct, st);
+  if (need && product_fp4_supported(p)) return launch_product_fp4(p, ws, st);
+  if (need) NVFP4_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(int), st));   // the status word
+  return launch_general(p, st);
 }
 
 }  // namespace
@@ -494,36 +451,43 @@ using namespace nvfp4;
 
 extern "C" {
 
+size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_in) {
+  if (!product_fp4_shape(n_rows, d_in)) return 0;
+  return product_fp4_ws_bytes(n_rows, d_in);
+}
+
 nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const uint8_t* codes,
                         const uint8_t* scales, const float* global_scale, int64_t d_out,
-                        int64_t d_in, void* Y, nvfp4_dtype y_dtype, nvfp4_stream_t stream) {
+                        int64_t d_in, void* Y, nvfp4_dtype y_dtype, void* ws, size_t ws_bytes,
+                        nvfp4_stream_t stream) {
   const Matrix w[1] = {{codes, scales, global_scale}};
-  return product(X, x_dtype, n_tok, nullptr, nullptr, 1, n_tok, w, 1, d_out, d_in, Y, y_dtype,
-                 stream);
+  return product(X, x_dtype, n_tok, nullptr, nullptr, 1, n_tok, w, 1, d_out, d_in, Y, y_dtype, ws,
+                 ws_bytes, stream);
 }
 
 nvfp4_status nvfp4_gemv_swiglu(const void* X, nvfp4_dtype x_dtype, int64_t n_tok,
                                const uint8_t* gate_codes, const uint8_t* gate_scales,
                                const float* gate_global_scale, const uint8_t* up_codes,
                                const uint8_t* up_scales, const float* up_global_scale,
-                               int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype y_dtype,
-                               nvfp4_stream_t stream) {
+                               int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype y_dtype, void* ws,
+                               size_t ws_bytes, nvfp4_stream_t stream) {
   const Matrix w[2] = {{gate_codes, gate_scales, gate_global_scale},
                        {up_codes, up_scales, up_global_scale}};
-  return product(X, x_dtype, n_tok, nullptr, nullptr, 1, n_tok, w, 2, d_out, d_in, Y, y_dtype,
-                 stream);
+  return product(X, x_dtype, n_tok, nullptr, nullptr, 1, n_tok, w, 2, d_out, d_in, Y, y_dtype, ws,
+                 ws_bytes, stream);
 }
 
 nvfp4_status nvfp4_gemv_experts(const void* X, nvfp4_dtype x_dtype, int64_t n_x, const int32_t* rows,
                                 const int32_t* offsets, int64_t n_experts, int64_t n_rows,
                                 const uint8_t* codes, const uint8_t* scales,
                                 const float* global_scales, int64_t d_out, int64_t d_in, void* Y,
-                                nvfp4_dtype y_dtype, nvfp4_stream_t stream) {
+                                nvfp4_dtype y_dtype, void* ws, size_t ws_bytes,
+                                nvfp4_stream_t stream) {
   if (n_experts > 0 && n_rows > 0 && !offsets) return NVFP4_ERR_INVALID_ARG;
   if (!rows && n_x != n_rows) return NVFP4_ERR_INVALID_ARG;
   const Matrix w[1] = {{codes, scales, global_scales}};
   return product(X, x_dtype, n_x, rows, offsets, n_experts, n_rows, w, 1, d_out, d_in, Y, y_dtype,
-                 stream);
+                 ws, ws_bytes, stream);
 }
 
 nvfp4_status nvfp4_gemv_swiglu_experts(
@@ -531,13 +495,13 @@ nvfp4_status nvfp4_gemv_swiglu_experts(
     int64_t n_experts, int64_t n_rows, const uint8_t* gate_codes, const uint8_t* gate_scales,
     const float* gate_global_scales, const uint8_t* up_codes, const uint8_t* up_scales,
     const float* up_global_scales, int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype y_dtype,
-    nvfp4_stream_t stream) {
+    void* ws, size_t ws_bytes, nvfp4_stream_t stream) {
   if (n_experts > 0 && n_rows > 0 && !offsets) return NVFP4_ERR_INVALID_ARG;
   if (!rows && n_x != n_rows) return NVFP4_ERR_INVALID_ARG;
   const Matrix w[2] = {{gate_codes, gate_scales, gate_global_scales},
                        {up_codes, up_scales, up_global_scales}};
   return product(X, x_dtype, n_x, rows, offsets, n_experts, n_rows, w, 2, d_out, d_in, Y, y_dtype,
-                 stream);
+                 ws, ws_bytes, stream);
 }
 
 }  // extern "C"

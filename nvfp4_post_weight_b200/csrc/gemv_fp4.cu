@@ -1,0 +1,694 @@
+// Products of a few tokens with NVFP4 weights on the block-scaled FP4 tensor
+// cores: the codes and the block scales go to the matrix unit as they are
+// (tcgen05.mma kind::mxf4nvf4, 16-element blocks with E4M3 scales), and the
+// tokens are taken apart into FP4 digits instead.
+//
+// Digits: a 16-element block of a token is a fixed-point integer
+// v = rn(x 2^(21 - eb)), |v| <= 2^22, eb the exponent of the block's largest
+// entry, written with eight digits -4 .. 3 of base 8, all of them E2M1 values;
+// the block's power of two 2^(eb - E) (E: the token's largest exponent) is its
+// E4M3 scale.  Each token is eight columns of the product, and
+// x . q = 2^(E - 29) sum_p 8^p D_p.  The products are exact; a column is summed
+// in fp32 by the matrix unit.  An entry is kept to 2^-22 of the largest of its
+// block, or to 2^-39 of the token's largest (blocks more than 17 octaves below
+// it), so bf16 entries within 2^-14 of their block's largest are exact.
+//
+// The weights' bytes bound the product: nothing is decoded, a warp's lanes issue
+// the copies and one thread the matrix instructions.  One CTA per SM streams
+// rows of its own, equal to eight rows over all SMs, in tiles of 128 (an M =
+// 128 instruction may have rows that are not there: rows do not mix), 256
+// columns of K a stage.
+#include <cuda_bf16.h>
+#include <string.h>
+
+#include "gemv.cuh"
+#include "sm100.cuh"
+
+namespace nvfp4 {
+namespace {
+
+using namespace sm100;
+
+constexpr int kPanelK = 256;                      // columns of K in a 128-byte row of codes
+constexpr int kMaxPanels = 4;                     // panels per stage
+constexpr int kMaxStages = 12;
+constexpr int kWorkers = 8;                       // warps that move scales and read sums
+constexpr int kThreads = (kWorkers + 3) * 32;
+constexpr int64_t kMaxRows = 2048;                // sorted rows that are taken apart at a time
+constexpr int kTile = 128;
+constexpr int kUnit = 8;                          // output columns that are shared out together
+constexpr int kSmem = 225 * 1024;
+constexpr int kTmemCols = 512;                    // sums, then buffers of a stage's scales
+constexpr int kNonFinite = 0x7FFFFFFF;            // in place of a token's exponent
+
+struct Fp4Args {
+  // codes and scales of each matrix in boxes of tile and of 32 rows by one stage
+  CUtensorMap codes[2][2], scales[2][2];
+  Product p;
+  const uint8_t* digits;    // per panel and sorted row: 8 x 128 bytes, 128-byte swizzle
+  const uint8_t* sf;        // per panel and sorted row: 16 scale codes
+  const int* expo;          // per sorted row: E or kNonFinite
+  int* status;
+  int panels;               // per stage
+  int n_stages;             // of K
+  int tokens;               // per pass
+  int tile;                 // output columns per accumulator, at most kTile
+  int ring;                 // stages of shared memory
+  int stage_bytes;
+  int d_bufs;               // accumulators
+  int sf_bufs;              // buffers of scales in tensor memory (at most ring)
+};
+
+// ---- the tokens' digits --------------------------------------------------------
+// CTA (r, part): sorted row r (zeros if it points outside X), 2048 columns.
+constexpr int kDigitCols = 2048;
+
+template <typename TX>
+__device__ __forceinline__ void load8(const TX* p, float* f) {
+  if constexpr (sizeof(TX) == 2) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      f[2 * j] = __uint_as_float(h[j] << 16);
+      f[2 * j + 1] = __uint_as_float(h[j] & 0xFFFF0000u);
+    }
+  } else {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+}
+
+// Exponent of a magnitude's bits (subnormals as the least normal one).
+__device__ __forceinline__ int exponent(uint32_t bits) {
+  return max((int)(bits >> 23), 1) - 127;
+}
+
+// Row of X of sorted row r, or -1.
+__device__ __forceinline__ int64_t x_row(const Product& p, int64_t r) {
+  if (!p.rows) return r;
+  const int64_t x = __ldg(p.rows + r);
+  return x < p.n_x ? x : -1;
+}
+
+template <typename TX>
+__global__ void __launch_bounds__(256)
+    digits_kernel(const Product p, uint8_t* __restrict__ digits,
+                  uint8_t* __restrict__ sf, int* __restrict__ expo, int* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ uint32_t warp_max[8];
+  const int64_t r = blockIdx.x;
+  const int d_in = (int)p.d_in;
+  const int64_t row = x_row(p, r);
+  const TX* x = static_cast<const TX*>(p.X) + row * d_in;
+  if (r == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
+  // the row's largest magnitude (bits order like values; not finite: above all)
+  uint32_t big = 0;
+  if (row >= 0)
+    for (int k = threadIdx.x * 8; k < d_in; k += 256 * 8) {
+      float f[8];
+      load8(x + k, f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) big = max(big, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+    }
+  for (int d = 16; d > 0; d >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, d));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = big;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) big = max(big, warp_max[w]);
+  const bool finite = big < 0x7F800000u;
+  const int E = exponent(big);
+  if (blockIdx.y == 0 && threadIdx.x == 0) expo[r] = finite ? E : kNonFinite;
+  const int k = blockIdx.y * kDigitCols + threadIdx.x * 8;
+  if (k >= d_in) return;
+  float f[8] = {};
+  if (row >= 0 && finite) load8(x + k, f);
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));   // a block is two lanes' entries
+  const int below = min(E - exponent(most), 17);
+  const int up = 21 - (E - below);                 // 2^up in two factors of fp32's range
+  const float s0 = __uint_as_float((uint32_t)(up / 2 + 127) << 23);
+  const float s1 = __uint_as_float((uint32_t)(up - up / 2 + 127) << 23);
+  uint32_t u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // rounded to an integer by the addition (|v| <= 2^22), then made a sum of
+    // digits 0 .. 7 by adding 4 at every place
+    const float v = __fadd_rn(f[j] * s0 * s1, 0x1.8p23f);
+    u[j] = __float_as_uint(v) - 0x4B400000u + 9586980u;
+  }
+  const int panel = k / kPanelK, byte = (k % kPanelK) / 2;
+  const int64_t at = panel * p.n_rows + r;
+  uint8_t* out = digits + at * 1024;
+#pragma unroll
+  for (int p = 0; p < 8; ++p) {
+    uint32_t word = 0;   // E2M1 codes of -4 .. 3, first element lowest
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      word |= ((0x5420ACDEu >> (4 * (u[j] >> (3 * p) & 7u))) & 0xFu) << (4 * j);
+    *reinterpret_cast<uint32_t*>(out + p * 128 + ((((byte >> 4) ^ p) & 7) << 4) + (byte & 15)) =
+        word;
+  }
+  if ((threadIdx.x & 1) == 0) {
+    // 2^(8 - below) in E4M3: normal down to 2^-6, then 2^-7, 2^-8, 2^-9
+    const int code = below <= 14 ? (15 - below) << 3 : 4 >> (below - 15);
+    sf[at * 16 + (k % kPanelK) / 16] = (uint8_t)code;
+  }
+}
+
+// ---- the product -----------------------------------------------------------------
+struct Shared {
+  uint64_t weights[kMaxStages];   // codes and scales of a stage have landed
+  uint64_t tokens[kMaxStages];    // its digits have
+  uint64_t scaled[kMaxStages];    // its scales are in tensor memory
+  uint64_t empty[kMaxStages];     // its matrix instructions are done
+  uint64_t d_full[2], d_empty[2]; // an accumulator is complete, has been read
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ void give_up(Shared* sh, int* status) {
+  atomicExch(&sh->abort, 1);
+  pdl_wait();   // (the kernel before this one clears the word)
+  atomicCAS(status, 0, (int)NVFP4_ERR_TIMEOUT);
+}
+__device__ __forceinline__ bool aborted(Shared* sh) {
+  return *reinterpret_cast<volatile int*>(&sh->abort) != 0;
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+// The pipeline waits of sm100.cuh with the limit read once; given up too when
+// another role has.  Warp-wide (so that what follows stays warp-uniform and the
+// matrix instructions' operands in uniform registers).
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned long long limit,
+                                     Shared* sh) {
+  bool ok = limit <= 1 ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const uint64_t t0 = globaltimer();
+    while (!ok && limit > 1 && !aborted(sh) && globaltimer() - t0 <= limit)
+      for (int i = 0; i < 16 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
+}
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// 16 (4) consecutive columns of this thread's TMEM lane (warp-wide).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint4* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z),
+      "r"(v[1].w), "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y),
+      "r"(v[3].z), "r"(v[3].w)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint4& v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                            int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// What one CTA works through: pieces of (expert, pass over its tokens), each a
+// range of output columns.
+struct Piece {
+  int e, t0, n;             // expert, its first sorted row and their number in this pass
+  int64_t row0, row1;       // output columns
+};
+struct Pieces {
+  int64_t u, u_end, units;
+  __device__ __forceinline__ void init(const Fp4Args& a) {
+    units = (a.p.d_out + kUnit - 1) / kUnit;
+    const int64_t all = count_passes(a.p, a.tokens) * units;
+    u = all * blockIdx.x / gridDim.x;
+    u_end = all * (blockIdx.x + 1) / gridDim.x;
+  }
+  // Warp-wide.
+  __device__ __forceinline__ bool next(const Fp4Args& a, Piece* q) {
+    if (u >= u_end) return false;
+    const int64_t slot = u / units, ub = u - slot * units;
+    const int64_t ue = min(units, u_end - slot * units);
+    u = slot * units + ue;
+    find_pass(a.p, a.tokens, (int)slot, &q->e, &q->t0, &q->n);
+    q->row0 = ub * kUnit;
+    q->row1 = min(ue * kUnit, a.p.d_out);
+    return true;
+  }
+};
+
+// One product x . q by plain sums: row x of X, column o of matrix w of expert e.
+// For tokens that digits cannot stand for (a NaN or an infinity among them).
+__device__ __noinline__ float plain_product(const Product& p, int w, int e, int64_t x, int64_t o) {
+  const int64_t block = (e * p.d_out + o) * p.nb;
+  const uint2* codes = reinterpret_cast<const uint2*>(p.codes[w]) + block;
+  float sum = 0.f;
+  for (int b = 0; b < p.nb; ++b) {
+    const uint2 c = codes[b];
+    const float scale = (float)e4m3_value(p.scales[w][block + b] & 0x7F);
+    for (int j = 0; j < kBlock; ++j) {
+      const int64_t k = x * p.d_in + b * kBlock + j;
+      const float v = p.x_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.X)[k])
+                               : static_cast<const float*>(p.X)[k];
+      sum = fmaf(v, e2m1_value((j < 8 ? c.x : c.y) >> (4 * (j & 7)) & 0xF) * scale, sum);
+    }
+  }
+  return sum * p.sg[w][e];
+}
+
+template <int NW>
+__global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_constant__ Fp4Args a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~uintptr_t(1023));
+  __shared__ Shared shared;
+  Shared* sh = &shared;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = a.panels, S = a.ring, K = a.n_stages;
+  const int columns = (a.tokens + 1) / 2 * 16;   // of an accumulator, per matrix
+  const int blocks = columns > 128 ? 2 : 1;      // 128-row groups of the digits' scales
+  const int sf_cols = (NW + blocks) * 16 * P;    // TMEM columns of a stage's scales
+  // a stage: codes (matrix, panel, row), digits (panel, token), scales of the
+  // codes (matrix, row, panel), scales of the digits (panel, token).  (A matrix
+  // instruction reads 128 rows of codes, also where a tile has fewer: what
+  // follows them in shared memory, which only rows that are not written see.)
+  const int panel_bytes = a.tile * 128;
+  const int b_at = NW * P * panel_bytes, sfa_at = b_at + P * columns * 128;
+  const int sfb_at = sfa_at + NW * a.tile * 16 * P;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&sh->weights[s], 1);
+      mbar_init(&sh->tokens[s], 1);
+      mbar_init(&sh->scaled[s], kWorkers);
+      mbar_init(&sh->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->d_full[i], 1);
+      mbar_init(&sh->d_empty[i], kWorkers);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWorkers + 1) tmem_alloc(&sh->tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem;
+  const unsigned long long limit = __ldg(&g_wait_limit_ns);
+
+  Pieces pieces;
+  pieces.init(a);
+  Piece q;
+  int s = 0;          // slot of shared memory and its phase
+  uint32_t ph = 0;
+  auto step = [&] {
+    if (++s == S) s = 0, ph ^= 1;
+  };
+  // a copying role ends early: lets its copies issued so far land before the CTA exits
+  auto drain_copies = [&](uint64_t* bars, int issued) {
+    give_up(sh, a.status);
+    for (int k = 0; k < S && k < issued; ++k) {
+      if (--s < 0) s = S - 1, ph ^= 1;
+      mbar_wait_drain(&bars[s], ph);
+    }
+  };
+
+  if (warp == kWorkers) {
+    // ---------------------------------------------------------------- codes and their scales
+    int issued = 0;
+    bool ok = true;
+    while (ok && pieces.next(a, &q)) {
+      for (int64_t row = q.row0; ok && row < q.row1; row += a.tile) {
+        // a tile is one box (rows past the piece's end are not used); of experts a
+        // part of a tile takes boxes of 32 rows and one panel
+        const int valid = (int)min(q.row1 - row, (int64_t)a.tile);
+        const int part = a.p.offsets && valid <= a.tile - 32 ? 1 : 0;
+        const int step_rows = part ? 32 : a.tile, boxes = (valid + step_rows - 1) / step_rows;
+        const int ops = part ? P : 1;
+        const uint32_t bytes = (uint32_t)(NW * boxes * step_rows * (128 + 16) * P);
+        const int y = (int)(q.e * a.p.d_out + row);
+        for (int st = 0; st < K; ++st) {
+          ok = wait(&sh->empty[s], ph ^ 1, limit, sh);
+          if (!ok) break;
+          uint8_t* stage = stages + s * a.stage_bytes;
+          uint64_t* bar = &sh->weights[s];
+          if (elect()) {
+            mbar_arrive_expect_tx(bar, bytes);
+            for (int b = 0; b < boxes; ++b) {
+              const int off = b * step_rows;
+#pragma unroll
+              for (int m = 0; m < NW; ++m) {
+                for (int p = 0; p < ops; ++p)
+                  tma_load_3d(stage + (m * P + p) * panel_bytes + off * 128, &a.codes[m][part], bar,
+                              0, y + off, st * P + p);
+                tma_load_2d(stage + sfa_at + (m * a.tile + off) * 16 * P, &a.scales[m][part], bar,
+                            st * 16 * P, y + off);
+              }
+            }
+          }
+          __syncwarp();
+          ++issued;
+          step();
+        }
+      }
+    }
+    if (!ok) drain_copies(sh->weights, issued);
+  } else if (warp == kWorkers + 2) {
+    // ---------------------------------------------------------------- digits
+    pdl_wait();
+    int issued = 0;
+    bool ok = true;
+    while (ok && pieces.next(a, &q)) {
+      const uint32_t bytes = (uint32_t)(q.n * (1024 + 16) * P);
+      const int64_t next_d = a.p.n_rows * 1024, next_s = a.p.n_rows * 16;
+      for (int64_t row = q.row0; ok && row < q.row1; row += a.tile) {
+        const uint8_t *d = a.digits + (int64_t)q.t0 * 1024, *f = a.sf + (int64_t)q.t0 * 16;
+        for (int st = 0; st < K; ++st) {
+          ok = wait(&sh->empty[s], ph ^ 1, limit, sh);
+          if (!ok) break;
+          uint8_t* stage = stages + s * a.stage_bytes;
+          uint64_t* bar = &sh->tokens[s];
+          if (elect()) {
+            mbar_arrive_expect_tx(bar, bytes);
+            for (int p = 0; p < P; ++p) {
+              bulk_load(stage + b_at + p * columns * 128, d + p * next_d, q.n * 1024, bar);
+              bulk_load(stage + sfb_at + p * a.tokens * 16, f + p * next_s, q.n * 16, bar);
+            }
+          }
+          __syncwarp();
+          d += P * next_d;
+          f += P * next_s;
+          ++issued;
+          step();
+        }
+      }
+    }
+    if (!ok) drain_copies(sh->tokens, issued);
+  } else if (warp == kWorkers + 1) {
+    // ---------------------------------------------------------------- matrix instructions
+    int g = 0, sf = 0;   // accumulators so far, buffer of scales
+    bool ok = true;
+    while (ok && pieces.next(a, &q)) {
+      // E2M1 x E2M1, E4M3 scales, M = 128
+      const int cols = (q.n + 1) / 2 * 16;
+      const uint32_t idesc = (1u << 7) | (1u << 10) | ((uint32_t)(cols >> 3) << 17) | (1u << 27);
+      for (int64_t row = q.row0; ok && row < q.row1; row += a.tile, ++g) {
+        const int buf = a.d_bufs == 2 ? g & 1 : 0, use = a.d_bufs == 2 ? g >> 1 : g;
+        ok = wait(&sh->d_empty[buf], (use & 1) ^ 1, limit, sh);
+        tc_fence_after();
+        const uint32_t d = tmem + buf * NW * columns;
+        for (int st = 0; ok && st < K; ++st) {
+          ok = wait(&sh->scaled[s], ph, limit, sh) && wait(&sh->weights[s], ph, limit, sh) &&
+               wait(&sh->tokens[s], ph, limit, sh);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t stage = smem_u32(stages) + s * a.stage_bytes;
+          uint64_t da = smem_desc_sw128(stage, 16, 1024);
+          uint64_t db = smem_desc_sw128(stage + b_at, 16, 1024);
+          uint32_t sfa = tmem + a.d_bufs * NW * columns + sf * sf_cols;
+          uint32_t sfb = sfa + NW * P * 16;
+          if (++sf == a.sf_bufs) sf = 0;
+          if (elect()) {
+            for (int p = 0; p < P; ++p) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int m = 0; m < NW; ++m)
+                  mma_nvfp4(d + m * columns, da + (m * P * panel_bytes + 32 * k) / 16,
+                            db + 32 * k / 16, idesc, sfa + (m * P * 4 + k) * 4, sfb + k * blocks * 4,
+                            (uint32_t)(st | p | k));
+              da += panel_bytes / 16;
+              db += columns * 128 / 16;
+              sfa += 16;
+              sfb += blocks * 16;
+            }
+            mma_commit(&sh->empty[s]);
+          }
+          __syncwarp();
+          step();
+        }
+        if (ok && elect()) mma_commit(&sh->d_full[buf]);
+        __syncwarp();
+      }
+    }
+    if (!ok) give_up(sh, a.status);
+    // every instruction above completes before TMEM is released
+    if (elect()) mma_commit(&sh->drain);
+    __syncwarp();
+    mbar_wait_drain(&sh->drain, 0);
+  } else {
+    // ---------------------------------------------------------------- scales, sums
+    // Two groups of four warps, one warp per quarter of TMEM's lanes: lane l of
+    // each quarter gets, per 64 columns of K, the words of rows l, l + 32, l + 64
+    // and l + 96.  With two matrices group h brings the scales of matrix h, with
+    // one of every other panel; the digits' scales of a panel fall to the group
+    // that has less to do.
+    const int r = threadIdx.x & (kTile - 1), half = threadIdx.x >> 7;
+    const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
+    pdl_wait();   // (for the tokens' exponents)
+    int stage_no = 0, sf = 0, os = 0;   // stages so far, buffer of scales, its last stage's slot
+    uint32_t oph = 0;
+    auto get = [&](const uint8_t* p, int bytes_apart, uint4* v) {
+      uint4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[j] = *reinterpret_cast<const uint4*>(p + j * bytes_apart);
+        x[j].x &= 0x7F7F7F7Fu, x[j].y &= 0x7F7F7F7Fu, x[j].z &= 0x7F7F7F7Fu, x[j].w &= 0x7F7F7F7Fu;
+      }
+      v[0] = make_uint4(x[0].x, x[1].x, x[2].x, x[3].x);
+      v[1] = make_uint4(x[0].y, x[1].y, x[2].y, x[3].y);
+      v[2] = make_uint4(x[0].z, x[1].z, x[2].z, x[3].z);
+      v[3] = make_uint4(x[0].w, x[1].w, x[2].w, x[3].w);
+    };
+    int g = 0;
+    bool ok = true;
+    while (ok && pieces.next(a, &q)) {
+      for (int64_t row = q.row0; ok && row < q.row1; row += a.tile, ++g) {
+        for (int st = 0; st < K; ++st) {
+          // the buffer in TMEM is free when the instructions that read it last are
+          // done (a slot is only refilled after that too)
+          ok = wait(&sh->weights[s], ph, limit, sh) && wait(&sh->tokens[s], ph, limit, sh);
+          if (a.sf_bufs < S && stage_no >= a.sf_bufs) {
+            ok = ok && wait(&sh->empty[os], oph, limit, sh);
+            if (++os == S) os = 0, oph ^= 1;
+          }
+          if (!ok) break;
+          const uint8_t* stage = stages + s * a.stage_bytes;
+          const uint32_t sfa = quarter + tmem + a.d_bufs * NW * columns + sf * sf_cols;
+          const uint32_t sfb = sfa + NW * P * 16;
+          uint4 v[4];
+          for (int p = 0; p < P; ++p) {
+            const int m = NW == 2 ? half : 0;
+            if (NW == 2 || (p & 1) == half) {
+              get(stage + sfa_at + ((m * a.tile + lane) * P + p) * 16, 32 * 16 * P, v);
+              tmem_st16(sfa + (m * P + p) * 16, v);
+            }
+            if ((NW == 2 ? p & 1 : ~p & 1) == half) {
+              for (int b = 0; b < blocks; ++b) {   // a token has eight columns
+                get(stage + sfb_at + (p * a.tokens + b * 16 + (lane >> 3)) * 16, 4 * 16, v);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) tmem_st4(sfb + ((p * 4 + k) * blocks + b) * 4, v[k]);
+              }
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->scaled[s]);
+          ++stage_no;
+          if (++sf == a.sf_bufs) sf = 0;
+          step();
+        }
+        // the sums of the tile: thread = output column, every other token
+        const int buf = a.d_bufs == 2 ? g & 1 : 0, use = a.d_bufs == 2 ? g >> 1 : g;
+        ok = ok && wait(&sh->d_full[buf], use & 1, limit, sh);
+        if (!ok) {
+          give_up(sh, a.status);
+          break;
+        }
+        tc_fence_after();
+        const int64_t o = row + r, o_end = min(row + a.tile, q.row1);
+        const uint32_t d = tmem + quarter + buf * NW * columns;
+        for (int i = half; i < q.n; i += 2) {
+          const int E = __ldg(a.expo + q.t0 + i);
+          float v[NW];
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            float c[8];
+            tmem_ld8(d + w * columns + 8 * i, c);
+            float sum = c[7];
+#pragma unroll
+            for (int p = 6; p >= 0; --p) sum = fmaf(sum, 8.f, c[p]);
+            if (o < o_end) {
+              const double scale = __hiloint2double((E - 29 + 1023) << 20, 0);
+              v[w] = E == kNonFinite
+                         ? plain_product(a.p, w, q.e, x_row(a.p, q.t0 + i), o)
+                         : (float)((double)sum * (scale * (double)__ldg(a.p.sg[w] + q.e)));
+            }
+          }
+          if (o < o_end) write_product<NW>(a.p, v, q.t0 + i, o);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->d_empty[buf]);
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == kWorkers + 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+int panels_of(int64_t d_in) { return (int)(d_in / kPanelK); }
+
+}  // namespace
+
+bool product_fp4_shape(int64_t n_rows, int64_t d_in) {
+  return d_in % kPanelK == 0 && d_in > 0 && n_rows > 0 && n_rows <= kMaxRows;
+}
+
+size_t product_fp4_ws_bytes(int64_t n_rows, int64_t d_in) {
+  const size_t rows = n_rows, n = panels_of(d_in);
+  return kWsHeader + align256(rows * sizeof(int)) + align256(rows * n * 16) + rows * n * 1024;
+}
+
+bool product_fp4_supported(const Product& p) {
+  bool ok = product_fp4_shape(p.n_rows, p.d_in) && p.n_experts * p.d_out < (int64_t(1) << 31);
+  for (int m = 0; m < p.n_w; ++m)
+    ok = ok && (reinterpret_cast<uintptr_t>(p.codes[m]) & 15) == 0 &&
+         (reinterpret_cast<uintptr_t>(p.scales[m]) & 15) == 0;
+  return ok;
+}
+
+nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
+  Fp4Args a;
+  memset(&a, 0, sizeof(a));
+  a.p = p;
+  const int n_panels = panels_of(p.d_in);
+  char* w = static_cast<char*>(ws);
+  const size_t rows = p.n_rows;
+  a.status = reinterpret_cast<int*>(w);
+  w += kWsHeader;
+  int* expo = reinterpret_cast<int*>(w);
+  w += align256(rows * sizeof(int));
+  uint8_t* sf = reinterpret_cast<uint8_t*>(w);
+  w += align256(rows * n_panels * 16);
+  uint8_t* digits = reinterpret_cast<uint8_t*>(w);
+  a.expo = expo;
+  a.sf = sf;
+  a.digits = digits;
+  const dim3 grid((unsigned)p.n_rows, (unsigned)((p.d_in + kDigitCols - 1) / kDigitCols));
+  if (p.x_bf16)
+    digits_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, digits, sf, expo, a.status);
+  else
+    digits_kernel<float><<<grid, 256, 0, st>>>(p, digits, sf, expo, a.status);
+  NVFP4_LAUNCH_CHECK();
+  // tokens per pass: what the accumulators hold, in equal passes; for experts
+  // 16, so that an expert's rows of a small batch take one pass
+  const int most = p.n_w == 2 ? 24 : 32;
+  if (p.offsets) {
+    a.tokens = p.n_rows < 16 ? (int)p.n_rows : 16;
+  } else {
+    const int64_t passes = (p.n_rows + most - 1) / most;
+    a.tokens = (int)((p.n_rows + passes - 1) / passes);
+  }
+  const int columns = (a.tokens + 1) / 2 * 16;
+  const int64_t units = (p.d_out + kUnit - 1) / kUnit;
+  const int64_t slots = p.offsets ? (p.n_experts < p.n_rows ? p.n_experts : p.n_rows)
+                                  : (p.n_rows + a.tokens - 1) / a.tokens;
+  const int64_t ctas = units * slots < num_sms() ? units * slots : num_sms();
+  // equal tiles for the largest share of a CTA (experts': in steps of 32, see the copies)
+  const int64_t share = (units * slots + ctas - 1) / ctas * kUnit;
+  const int64_t tiles = (share + kTile - 1) / kTile, grain = p.offsets ? 32 : kUnit;
+  a.tile = (int)(((share + tiles - 1) / tiles + grain - 1) / grain * grain);
+  // panels per stage: as many as leave a ring of four stages (a stage costs each
+  // role a few hundred cycles whatever its size)
+  for (a.panels = kMaxPanels; a.panels >= 1; a.panels /= 2) {
+    // (the digits' scales are read for whole groups of 16 tokens)
+    a.stage_bytes = (a.panels * (p.n_w * a.tile * (128 + 16) + columns * 128 + a.tokens * 16) +
+                     32 * 16 + 1023) / 1024 * 1024;
+    a.ring = (kSmem - 1024 - kTile * 128) / a.stage_bytes;
+    const int sf_cols = (p.n_w + (columns > 128 ? 2 : 1)) * 16 * a.panels;
+    a.d_bufs = 2 * p.n_w * columns + 2 * sf_cols <= kTmemCols ? 2 : 1;
+    a.sf_bufs = (kTmemCols - a.d_bufs * p.n_w * columns) / sf_cols;
+    if (n_panels % a.panels == 0 && ((a.ring >= 4 && a.sf_bufs >= 2) || a.panels == 1)) break;
+  }
+  if (a.ring > kMaxStages) a.ring = kMaxStages;
+  if (a.sf_bufs > a.ring) a.sf_bufs = a.ring;
+  a.n_stages = n_panels / a.panels;
+  const uint64_t rows_w = (uint64_t)(p.n_experts * p.d_out), pitch = (uint64_t)p.d_in / 2;
+  for (int m = 0; m < p.n_w; ++m)
+    for (int b = 0; b < 2; ++b) {
+      const uint32_t box_rows = b == 0 ? a.tile : 32;
+      const uint64_t dc[3] = {128, rows_w, (uint64_t)n_panels}, sc[2] = {pitch, 128};
+      const uint32_t bc[3] = {128, box_rows, b == 0 ? (uint32_t)a.panels : 1u};
+      const uint64_t ds[2] = {(uint64_t)p.nb, rows_w}, ss[1] = {(uint64_t)p.nb};
+      const uint32_t bs[2] = {16u * a.panels, box_rows};
+      if (!encode_tmap_nd(&a.codes[m][b], p.codes[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dc, sc, bc,
+                          CU_TENSOR_MAP_SWIZZLE_128B) ||
+          !encode_tmap_2d(&a.scales[m][b], p.scales[m], CU_TENSOR_MAP_DATA_TYPE_UINT8, ds, ss, bs,
+                          CU_TENSOR_MAP_SWIZZLE_NONE))
+        return NVFP4_ERR_CUDA;
+    }
+  auto kernel = p.n_w == 2 ? product_fp4_kernel<2> : product_fp4_kernel<1>;
+  NVFP4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
+  NVFP4_CUDA_TRY(launch_chained(kernel, dim3((unsigned)ctas), dim3(kThreads), kSmem, st, a));
+  count_launches(2);
+  return NVFP4_OK;
+}
+
+}  // namespace nvfp4

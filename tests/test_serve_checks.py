@@ -12,12 +12,13 @@ OK, ARG, SHAPE = 0, 1, 2
 A = P(256)
 
 
-def gemv(X=A, xt=0, n=1, c=A, s=A, g=A, o=16, i=32, Y=A, yt=0):
-    return B.lib().nvfp4_gemv(X, xt, n, c, s, g, o, i, Y, yt, None)
+def gemv(X=A, xt=0, n=1, c=A, s=A, g=A, o=16, i=32, Y=A, yt=0, ws=None, nws=0):
+    return B.lib().nvfp4_gemv(X, xt, n, c, s, g, o, i, Y, yt, ws, nws, None)
 
 
 def experts(X=A, xt=0, n_x=4, rows=A, off=A, E=2, n=4, c=A, s=A, g=A, o=16, i=32, Y=A, yt=0):
-    return B.lib().nvfp4_gemv_experts(X, xt, n_x, rows, off, E, n, c, s, g, o, i, Y, yt, None)
+    return B.lib().nvfp4_gemv_experts(X, xt, n_x, rows, off, E, n, c, s, g, o, i, Y, yt, None, 0,
+                                      None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -33,11 +34,20 @@ def test_gemv_refuses(kw, status):
 
 def test_gemv_swiglu_refuses():
     f = B.lib().nvfp4_gemv_swiglu
-    assert f(A, 0, 1, A, A, A, None, A, A, 16, 32, A, 0, None) == ARG
-    assert f(A, 0, 1, A, A, A, A, A, None, 16, 32, A, 0, None) == ARG
-    assert f(A, 0, 1, A, A, A, P(260), A, A, 16, 32, A, 0, None) == ARG
-    assert f(A, 0, 1, A, A, A, A, A, A, 16, 40, A, 0, None) == SHAPE
-    assert f(A, 0, 0, A, A, A, A, A, A, 16, 32, A, 0, None) == OK
+    assert f(A, 0, 1, A, A, A, None, A, A, 16, 32, A, 0, None, 0, None) == ARG
+    assert f(A, 0, 1, A, A, A, A, A, None, 16, 32, A, 0, None, 0, None) == ARG
+    assert f(A, 0, 1, A, A, A, P(260), A, A, 16, 32, A, 0, None, 0, None) == ARG
+    assert f(A, 0, 1, A, A, A, A, A, A, 16, 40, A, 0, None, 0, None) == SHAPE
+    assert f(A, 0, 0, A, A, A, A, A, A, 16, 32, A, 0, None, 0, None) == OK
+
+
+def test_gemv_refuses_a_missing_or_small_workspace():
+    need = B.nvfp4_gemv_workspace_size(3, 512)
+    assert need > 3 * 512 * 4 and B.nvfp4_gemv_workspace_size(3, 32) == 0
+    assert B.lib().nvfp4_gemv_workspace_size(-1, 512) == 0
+    for kw in (dict(), dict(ws=A, nws=need - 1), dict(ws=P(128), nws=need)):
+        assert gemv(n=3, i=512, **kw) == 3
+    assert gemv(n=0, i=512) == OK
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -52,7 +62,7 @@ def test_gemv_experts_refuses(kw, status):
     d.update(kw)
     assert L.nvfp4_gemv_swiglu_experts(d["X"], d["xt"], d["n_x"], d["rows"], d["off"], d["E"],
                                        d["n"], A, A, A, A, A, A, d["o"], d["i"], d["Y"], d["yt"],
-                                       None) == status
+                                       None, 0, None) == status
 
 
 def test_routing_calls_refuse():
