@@ -30,9 +30,10 @@ namespace {
 using namespace sm100;
 
 constexpr int kPanelK = 256;                      // columns of K in a 128-byte row of codes
-constexpr int kMaxPanels = 4;                     // panels per stage
+constexpr int kMaxPanels = 2;                     // panels per stage
 constexpr int kMaxStages = 12;
-constexpr int kWorkers = 8;                       // warps that move scales and read sums
+constexpr int kGroups = 3;                        // groups of four warps that move scales and
+constexpr int kWorkers = 4 * kGroups;             // read sums
 constexpr int kThreads = (kWorkers + 3) * 32;
 constexpr int64_t kMaxRows = 2048;                // sorted rows that are taken apart at a time
 constexpr int kTile = 128;
@@ -60,8 +61,8 @@ struct Fp4Args {
 };
 
 // ---- the tokens' digits --------------------------------------------------------
-// CTA (r, part): sorted row r (zeros if it points outside X), 2048 columns.
-constexpr int kDigitCols = 2048;
+// CTA (r, part): sorted row r (zeros if it points outside X), 4096 columns.
+constexpr int kDigitThreads = 512, kDigitCols = kDigitThreads * 8;
 
 template <typename TX>
 __device__ __forceinline__ void load8(const TX* p, float* f) {
@@ -93,11 +94,11 @@ __device__ __forceinline__ int64_t x_row(const Product& p, int64_t r) {
 }
 
 template <typename TX>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kDigitThreads)
     digits_kernel(const Product p, uint8_t* __restrict__ digits,
                   uint8_t* __restrict__ sf, int* __restrict__ expo, int* status) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ uint32_t warp_max[8];
+  __shared__ uint32_t warp_max[kDigitThreads / 32];
   const int64_t r = blockIdx.x;
   const int d_in = (int)p.d_in;
   const int64_t row = x_row(p, r);
@@ -106,7 +107,8 @@ __global__ void __launch_bounds__(256)
   // the row's largest magnitude (bits order like values; not finite: above all)
   uint32_t big = 0;
   if (row >= 0)
-    for (int k = threadIdx.x * 8; k < d_in; k += 256 * 8) {
+#pragma unroll 4
+    for (int k = threadIdx.x * 8; k < d_in; k += kDigitThreads * 8) {
       float f[8];
       load8(x + k, f);
 #pragma unroll
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(256)
   if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = big;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 8; ++w) big = max(big, warp_max[w]);
+  for (int w = 0; w < kDigitThreads / 32; ++w) big = max(big, warp_max[w]);
   const bool finite = big < 0x7F800000u;
   const int E = exponent(big);
   if (blockIdx.y == 0 && threadIdx.x == 0) expo[r] = finite ? E : kNonFinite;
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
     for (int s = 0; s < kMaxStages; ++s) {
       mbar_init(&sh->weights[s], 1);
       mbar_init(&sh->tokens[s], 1);
-      mbar_init(&sh->scaled[s], kWorkers);
+      mbar_init(&sh->scaled[s], 4);
       mbar_init(&sh->empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -449,11 +451,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
         ok = wait(&sh->d_empty[buf], (use & 1) ^ 1, limit, sh);
         tc_fence_after();
         const uint32_t d = tmem + buf * NW * columns;
+        bool ready = false;
         for (int st = 0; ok && st < K; ++st) {
-          ok = wait(&sh->scaled[s], ph, limit, sh) && wait(&sh->weights[s], ph, limit, sh) &&
-               wait(&sh->tokens[s], ph, limit, sh);
+          // (the group that wrote the scales has waited for the stage's copies)
+          ok = ready || wait(&sh->scaled[s], ph, limit, sh);
           if (!ok) break;
           tc_fence_after();
+          // the next stage is looked at now: behind this one's instructions the look
+          // would queue for their issue
+          const int s1 = s + 1 == S ? 0 : s + 1;
+          ready = st + 1 < K && limit > 1 && mbar_test_wait(&sh->scaled[s1], s1 == 0 ? ph ^ 1 : ph);
+          ready = __all_sync(0xffffffffu, ready);
           const uint32_t stage = smem_u32(stages) + s * a.stage_bytes;
           uint64_t da = smem_desc_sw128(stage, 16, 1024);
           uint64_t db = smem_desc_sw128(stage + b_at, 16, 1024);
@@ -490,15 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
     mbar_wait_drain(&sh->drain, 0);
   } else {
     // ---------------------------------------------------------------- scales, sums
-    // Two groups of four warps, one warp per quarter of TMEM's lanes: lane l of
-    // each quarter gets, per 64 columns of K, the words of rows l, l + 32, l + 64
-    // and l + 96.  With two matrices group h brings the scales of matrix h, with
-    // one of every other panel; the digits' scales of a panel fall to the group
-    // that has less to do.
-    const int r = threadIdx.x & (kTile - 1), half = threadIdx.x >> 7;
+    // Groups of four warps, one warp per quarter of TMEM's lanes: lane l of each
+    // quarter gets, per 64 columns of K, the words of rows l, l + 32, l + 64 and
+    // l + 96.  A group takes the stages of its slots (a stage takes a group some
+    // 700 cycles, the matrix instructions 400; a slot's stages all fall to one
+    // group, which so sees each phase of its barriers), and every third token of a
+    // tile's sums.
+    const int r = threadIdx.x & (kTile - 1), group = threadIdx.x >> 7;
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
     pdl_wait();   // (for the tokens' exponents)
-    int stage_no = 0, sf = 0, os = 0;   // stages so far, buffer of scales, its last stage's slot
+    int stage_no = 0, sf = 0, os = 0;   // stages so far, buffer of scales, slot of its last stage
     uint32_t oph = 0;
     auto get = [&](const uint8_t* p, int bytes_apart, uint4* v) {
       uint4 x[4];
@@ -517,41 +526,41 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
     while (ok && pieces.next(a, &q)) {
       for (int64_t row = q.row0; ok && row < q.row1; row += a.tile, ++g) {
         for (int st = 0; st < K; ++st) {
+          const int slot = s, buf = sf, no = stage_no, free_slot = os;
+          const uint32_t phase = ph, free_phase = oph;
+          step();
+          ++stage_no;
+          if (++sf == a.sf_bufs) sf = 0;
+          if (no >= a.sf_bufs && ++os == S) os = 0, oph ^= 1;
+          if (slot % kGroups != group) continue;
           // the buffer in TMEM is free when the instructions that read it last are
-          // done (a slot is only refilled after that too)
-          ok = wait(&sh->weights[s], ph, limit, sh) && wait(&sh->tokens[s], ph, limit, sh);
-          if (a.sf_bufs < S && stage_no >= a.sf_bufs) {
-            ok = ok && wait(&sh->empty[os], oph, limit, sh);
-            if (++os == S) os = 0, oph ^= 1;
-          }
+          // done (where there are as many buffers as slots, the copies waited for it)
+          ok = wait(&sh->weights[slot], phase, limit, sh) && wait(&sh->tokens[slot], phase, limit, sh);
+          if (a.sf_bufs < S && no >= a.sf_bufs)
+            ok = ok && wait(&sh->empty[free_slot], free_phase, limit, sh);
           if (!ok) break;
-          const uint8_t* stage = stages + s * a.stage_bytes;
-          const uint32_t sfa = quarter + tmem + a.d_bufs * NW * columns + sf * sf_cols;
+          const uint8_t* stage = stages + slot * a.stage_bytes;
+          const uint32_t sfa = quarter + tmem + a.d_bufs * NW * columns + buf * sf_cols;
           const uint32_t sfb = sfa + NW * P * 16;
           uint4 v[4];
           for (int p = 0; p < P; ++p) {
-            const int m = NW == 2 ? half : 0;
-            if (NW == 2 || (p & 1) == half) {
+#pragma unroll
+            for (int m = 0; m < NW; ++m) {
               get(stage + sfa_at + ((m * a.tile + lane) * P + p) * 16, 32 * 16 * P, v);
               tmem_st16(sfa + (m * P + p) * 16, v);
             }
-            if ((NW == 2 ? p & 1 : ~p & 1) == half) {
-              for (int b = 0; b < blocks; ++b) {   // a token has eight columns
-                get(stage + sfb_at + (p * a.tokens + b * 16 + (lane >> 3)) * 16, 4 * 16, v);
+            for (int b = 0; b < blocks; ++b) {   // a token has eight columns
+              get(stage + sfb_at + (p * a.tokens + b * 16 + (lane >> 3)) * 16, 4 * 16, v);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_st4(sfb + ((p * 4 + k) * blocks + b) * 4, v[k]);
-              }
+              for (int k = 0; k < 4; ++k) tmem_st4(sfb + ((p * 4 + k) * blocks + b) * 4, v[k]);
             }
           }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->scaled[s]);
-          ++stage_no;
-          if (++sf == a.sf_bufs) sf = 0;
-          step();
+          if (lane == 0) mbar_arrive(&sh->scaled[slot]);
         }
-        // the sums of the tile: thread = output column, every other token
+        // the sums of the tile: thread = output column, the group's tokens
         const int buf = a.d_bufs == 2 ? g & 1 : 0, use = a.d_bufs == 2 ? g >> 1 : g;
         ok = ok && wait(&sh->d_full[buf], use & 1, limit, sh);
         if (!ok) {
@@ -561,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
         tc_fence_after();
         const int64_t o = row + r, o_end = min(row + a.tile, q.row1);
         const uint32_t d = tmem + quarter + buf * NW * columns;
-        for (int i = half; i < q.n; i += 2) {
+        for (int i = group; i < q.n; i += kGroups) {
           const int E = __ldg(a.expo + q.t0 + i);
           float v[NW];
 #pragma unroll
@@ -633,9 +642,9 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
   a.digits = digits;
   const dim3 grid((unsigned)p.n_rows, (unsigned)((p.d_in + kDigitCols - 1) / kDigitCols));
   if (p.x_bf16)
-    digits_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p, digits, sf, expo, a.status);
+    digits_kernel<__nv_bfloat16><<<grid, kDigitThreads, 0, st>>>(p, digits, sf, expo, a.status);
   else
-    digits_kernel<float><<<grid, 256, 0, st>>>(p, digits, sf, expo, a.status);
+    digits_kernel<float><<<grid, kDigitThreads, 0, st>>>(p, digits, sf, expo, a.status);
   NVFP4_LAUNCH_CHECK();
   // tokens per pass: what the accumulators hold, in equal passes; for experts
   // 16, so that an expert's rows of a small batch take one pass
@@ -655,20 +664,23 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
   const int64_t share = (units * slots + ctas - 1) / ctas * kUnit;
   const int64_t tiles = (share + kTile - 1) / kTile, grain = p.offsets ? 32 : kUnit;
   a.tile = (int)(((share + tiles - 1) / tiles + grain - 1) / grain * grain);
-  // panels per stage: as many as leave a ring of four stages (a stage costs each
-  // role a few hundred cycles whatever its size)
+  // panels per stage: two (a stage costs each role a few hundred cycles whatever its
+  // size) where that leaves a ring of three stages, or four for two matrices
   for (a.panels = kMaxPanels; a.panels >= 1; a.panels /= 2) {
     // (the digits' scales are read for whole groups of 16 tokens)
     a.stage_bytes = (a.panels * (p.n_w * a.tile * (128 + 16) + columns * 128 + a.tokens * 16) +
                      32 * 16 + 1023) / 1024 * 1024;
-    a.ring = (kSmem - 1024 - kTile * 128) / a.stage_bytes;
+    // (rows that a tile lacks are read behind the last stage too)
+    const int behind = (kTile - a.tile) * (128 + 16 * a.panels);
+    a.ring = (kSmem - 1024 - behind) / a.stage_bytes;
     const int sf_cols = (p.n_w + (columns > 128 ? 2 : 1)) * 16 * a.panels;
     a.d_bufs = 2 * p.n_w * columns + 2 * sf_cols <= kTmemCols ? 2 : 1;
     a.sf_bufs = (kTmemCols - a.d_bufs * p.n_w * columns) / sf_cols;
-    if (n_panels % a.panels == 0 && ((a.ring >= 4 && a.sf_bufs >= 2) || a.panels == 1)) break;
+    if (a.panels == 1 || (n_panels % a.panels == 0 && a.ring >= p.n_w + 2 && a.sf_bufs >= 3)) break;
   }
   if (a.ring > kMaxStages) a.ring = kMaxStages;
   if (a.sf_bufs > a.ring) a.sf_bufs = a.ring;
+  if (a.ring < 2 || a.sf_bufs < 1) return NVFP4_ERR_UNSUPPORTED;   // (three stages fit at least)
   a.n_stages = n_panels / a.panels;
   const uint64_t rows_w = (uint64_t)(p.n_experts * p.d_out), pitch = (uint64_t)p.d_in / 2;
   for (int m = 0; m < p.n_w; ++m)
