@@ -630,46 +630,63 @@ def nvfp4_layer_error_batched(Ws, codes, scales, global_scales, Hs, errs, ws, st
 # ---------------------------------------------------------------------------
 # products with the solved weights, and tokens by expert and back
 # ---------------------------------------------------------------------------
-def _stream_of(call, tensors, stream):
-    """The given stream, or the current one, of the device that the tensors
-    must share."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t.device != dev:
-            raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"tensors on {dev} and {t.device}")
-    if stream is None:
-        return torch.cuda.current_stream(dev)
-    if stream.device != dev:
+# (these calls may take a few microseconds on the device, so their checks first
+# ask what holds for good arguments and leave the message to _need)
+def _arg(call, t, name, shape, dtype, dev):
+    """Data pointer of a contiguous CUDA tensor of the given shape and dtype on
+    device number dev; raises Nvfp4Error otherwise."""
+    if (type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous()):
+        if t.get_device() == dev:
+            return t.data_ptr()
         raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG,
-                         f"stream of {stream.device}, tensors on {dev}")
-    return stream
+                         f"{name}: tensors on cuda:{dev} and {t.device}")
+    _need(call, t, name, shape, dtype)
+    if t.get_device() != dev:
+        raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG,
+                         f"{name}: tensors on cuda:{dev} and {t.device}")
+    return t.data_ptr()
 
 
-def _run_on(call, tensors, stream, *args):
-    """Calls the library on a stream of the tensors' device, with that device
-    current."""
-    stream = _stream_of(call, tensors, stream)
-    dev = tensors[0].device
+def _io_matrix(call, t, name):
+    """(rows, columns, library dtype, device number) of a contiguous bf16 or
+    fp32 CUDA matrix."""
+    if (type(t) is torch.Tensor and t.is_cuda and t.dim() == 2 and t.dtype in _IO_DTYPES
+            and t.is_contiguous()):
+        return *t.shape, NVFP4_BF16 if t.dtype is torch.bfloat16 else NVFP4_F32, t.get_device()
+    rows, cols = _matrix(call, t, name, _IO_DTYPES)
+    return rows, cols, _dtype_code(t), t.get_device()
+
+
+def _run_on(call, dev, stream, *args):
+    """Calls the library on the given stream of device number dev (None: its
+    current one), with that device current."""
+    if stream is None:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    elif stream.device.index == dev:
+        raw = stream.cuda_stream
+    else:
+        raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG,
+                         f"stream of {stream.device}, tensors on cuda:{dev}")
     fn = getattr(lib(), call)
-    if dev.index == torch.cuda.current_device():
-        code = fn(*args, stream.cuda_stream)
+    if dev == torch.cuda.current_device():
+        code = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            code = fn(*args, stream.cuda_stream)
-    _check(call, code)
+            code = fn(*args, raw)
+    if code != 0:
+        raise Nvfp4Error(call, code)
 
 
-def _weight(call, name, w, lead, d_out, d_in):
-    """(codes, scales, global_scale) of one matrix (lead = ()) or of lead[0]
-    experts' matrices one after another."""
+def _weight(call, name, w, lead, d_out, d_in, dev):
+    """Pointers of (codes, scales, global_scale) of one matrix (lead = ()) or of
+    lead[0] experts' matrices one after another."""
     if len(w) != 3:
         raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"{name}: expected (codes, scales, "
                                                       f"global_scale)")
-    codes, scales, sg = w
-    _need(call, codes, name + "codes", (*lead, d_out, d_in // 2), _U8)
-    _need(call, scales, name + "scales", (*lead, d_out, d_in // 16), _U8)
-    _need(call, sg, name + ("global_scales" if lead else "global_scale"), lead or (1,), _F32)
-    return codes.data_ptr(), scales.data_ptr(), sg.data_ptr()
+    return (_arg(call, w[0], name + "codes", (*lead, d_out, d_in // 2), _U8, dev),
+            _arg(call, w[1], name + "scales", (*lead, d_out, d_in // 16), _U8, dev),
+            _arg(call, w[2], name + "global_scale", lead or (1,), _F32, dev))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -680,39 +697,37 @@ def nvfp4_gemv_workspace_size(n_rows, d_in) -> int:
 
 def _product(call, X, weights, Y, offsets, rows, ws, stream):
     """weights: [(name prefix, (codes, scales, global_scale))]."""
-    n_x, d_in = _matrix(call, X, "X", _IO_DTYPES)
-    n_rows, d_out = _matrix(call, Y, "Y", _IO_DTYPES)
-    tensors = [X, Y, *(t for _, w in weights for t in w)]
+    n_x, d_in, xt, dev = _io_matrix(call, X, "X")
+    n_rows, d_out, yt, y_dev = _io_matrix(call, Y, "Y")
+    if y_dev != dev:
+        raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"tensors on {X.device} and {Y.device}")
     if d_in % 16:
         raise Nvfp4Error(call, 2, f"X: {d_in} columns, not a multiple of 16")
+    if rows is None and n_rows != n_x:
+        raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"X has {n_x} rows, Y {n_rows}")
     if offsets is None:
-        if n_rows != n_x:
-            raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"X has {n_x} rows, Y {n_rows}")
         lead, head = (), ()
     else:
         _need(call, offsets, "offsets", dtype=_I32, numel_min=1)
-        _need(call, offsets, "offsets", (offsets.numel(),))
-        tensors.append(offsets)
-        if rows is None:
-            if n_rows != n_x:
-                raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG,
-                                 f"X has {n_x} rows, Y {n_rows}, and rows is missing")
-        else:
-            _need(call, rows, "rows", (n_rows,), _I32)
-            tensors.append(rows)
-        lead = (offsets.numel() - 1,)
-        head = (None if rows is None else rows.data_ptr(), offsets.data_ptr(), lead[0], n_rows)
-    w = [p for name, t in weights for p in _weight(call, name, t, lead, d_out, d_in)]
+        n = offsets.numel()
+        head = (None if rows is None else _arg(call, rows, "rows", (n_rows,), _I32, dev),
+                _arg(call, offsets, "offsets", (n,), _I32, dev), n - 1, n_rows)
+        lead = (n - 1,)
+    w = []
+    for name, t in weights:
+        w += _weight(call, name, t, lead, d_out, d_in, dev)
     nws = nvfp4_gemv_workspace_size(n_rows, d_in)
     if ws is not None:
         _ws_bytes(call, ws, nws)
-        tensors.append(ws)
+        pws, nws = _arg(call, ws, "workspace", ws.shape, _U8, dev), ws.numel()
     elif nws:   # from torch's pool of the stream it is used on
-        with on_stream(_stream_of(call, tensors, stream)):
-            ws = workspace(nws, X.device)
-    _run_on(call, tensors, stream, X.data_ptr(), _dtype_code(X), n_x, *head, *w, d_out, d_in,
-            Y.data_ptr(), _dtype_code(Y), None if ws is None else ws.data_ptr(),
-            0 if ws is None else ws.numel())
+        with on_stream(stream):
+            ws = torch.empty(nws, dtype=_U8, device=X.device)
+        pws = ws.data_ptr()
+    else:
+        pws = None
+    _run_on(call, dev, stream, X.data_ptr(), xt, n_x, *head, *w, d_out, d_in, Y.data_ptr(), yt, pws,
+            nws)
 
 
 def nvfp4_gemv(X, codes, scales, global_scale, Y, ws=None, stream=None):
@@ -768,51 +783,50 @@ def nvfp4_moe_sort(expert_ids, offsets, rows, position, stream=None):
     call = "nvfp4_moe_sort"
     n_tok, top_k = _matrix(call, expert_ids, "expert_ids", (_I32, torch.int64))
     _need(call, offsets, "offsets", dtype=_I32, numel_min=1)
-    _need(call, offsets, "offsets", (offsets.numel(),))
-    _need(call, rows, "rows", (n_tok * top_k,), _I32)
-    _need(call, position, "position", (n_tok, top_k), _I32)
-    _run_on(call, (expert_ids, offsets, rows, position), stream, expert_ids.data_ptr(),
-            expert_ids.element_size(), n_tok, top_k, offsets.numel() - 1, offsets.data_ptr(),
-            rows.data_ptr(), position.data_ptr())
+    dev, n = expert_ids.get_device(), offsets.numel()
+    _run_on(call, dev, stream, expert_ids.data_ptr(), expert_ids.element_size(), n_tok, top_k,
+            n - 1, _arg(call, offsets, "offsets", (n,), _I32, dev),
+            _arg(call, rows, "rows", (n_tok * top_k,), _I32, dev),
+            _arg(call, position, "position", (n_tok, top_k), _I32, dev))
+
+
+def _slots(call, position, n_tok, dev):
+    """(pointer, top_k) of position (n_tok, top_k)."""
+    if type(position) is not torch.Tensor or position.dim() != 2:
+        _matrix(call, position, "position", _I32)
+    top_k = position.shape[1]
+    return _arg(call, position, "position", (n_tok, top_k), _I32, dev), top_k
 
 
 def nvfp4_moe_gather(X, position, Xs, stream=None):
     """Xs[position[t, j]] = X[t]; rows that no slot names are left as they were."""
     call = "nvfp4_moe_gather"
-    n_tok, d = _matrix(call, X, "X", _IO_DTYPES)
-    n_pos, top_k = _matrix(call, position, "position", _I32)
-    _need(call, position, "position", (n_tok, top_k))
-    _need(call, Xs, "Xs", (n_tok * top_k, d), X.dtype)
-    _run_on(call, (X, position, Xs), stream, X.data_ptr(), _dtype_code(X), position.data_ptr(),
-            n_tok, top_k, d, Xs.data_ptr())
+    n_tok, d, xt, dev = _io_matrix(call, X, "X")
+    pos, top_k = _slots(call, position, n_tok, dev)
+    _run_on(call, dev, stream, X.data_ptr(), xt, pos, n_tok, top_k, d,
+            _arg(call, Xs, "Xs", (n_tok * top_k, d), X.dtype, dev))
 
 
 def nvfp4_moe_combine(Ys, position, Y, weights=None, stream=None):
     """Y[t] = sum_j weights[t, j] Ys[position[t, j]] (weights fp32, or None for
     1: the gradient of nvfp4_moe_gather)."""
     call = "nvfp4_moe_combine"
-    n_tok, d = _matrix(call, Y, "Y", _IO_DTYPES)
-    _, top_k = _matrix(call, position, "position", _I32)
-    _need(call, position, "position", (n_tok, top_k))
-    _need(call, Ys, "Ys", (n_tok * top_k, d), _IO_DTYPES)
-    _opt_need(call, weights, "weights", shape=(n_tok, top_k), dtype=_F32)
-    tensors = (Ys, position, Y) if weights is None else (Ys, position, Y, weights)
-    _run_on(call, tensors, stream, Ys.data_ptr(), _dtype_code(Ys), position.data_ptr(),
-            None if weights is None else weights.data_ptr(), n_tok, top_k, d, Y.data_ptr(),
-            _dtype_code(Y))
+    n_tok, d, yt, dev = _io_matrix(call, Y, "Y")
+    pos, top_k = _slots(call, position, n_tok, dev)
+    _, _, st, _ = _io_matrix(call, Ys, "Ys")
+    _run_on(call, dev, stream, _arg(call, Ys, "Ys", (n_tok * top_k, d), Ys.dtype, dev), st, pos,
+            None if weights is None else _arg(call, weights, "weights", (n_tok, top_k), _F32, dev),
+            n_tok, top_k, d, Y.data_ptr(), yt)
 
 
 def nvfp4_moe_combine_backward(dY, Ys, position, weights, dYs, dweights, stream=None):
     """Gradients of nvfp4_moe_combine: dYs[position[t, j]] = weights[t, j] dY[t],
     dweights[t, j] = <dY[t], Ys[position[t, j]]>."""
     call = "nvfp4_moe_combine_backward"
-    n_tok, d = _matrix(call, dY, "dY", _IO_DTYPES)
-    _, top_k = _matrix(call, position, "position", _I32)
-    _need(call, position, "position", (n_tok, top_k))
-    _need(call, Ys, "Ys", (n_tok * top_k, d), dY.dtype)
-    _need(call, dYs, "dYs", (n_tok * top_k, d), dY.dtype)
-    _need(call, weights, "weights", (n_tok, top_k), _F32)
-    _need(call, dweights, "dweights", (n_tok, top_k), _F32)
-    _run_on(call, (dY, Ys, position, weights, dYs, dweights), stream, dY.data_ptr(),
-            Ys.data_ptr(), _dtype_code(dY), position.data_ptr(), weights.data_ptr(), n_tok, top_k,
-            d, dYs.data_ptr(), dweights.data_ptr())
+    n_tok, d, dt, dev = _io_matrix(call, dY, "dY")
+    pos, top_k = _slots(call, position, n_tok, dev)
+    shape = (n_tok * top_k, d)
+    _run_on(call, dev, stream, dY.data_ptr(), _arg(call, Ys, "Ys", shape, dY.dtype, dev), dt, pos,
+            _arg(call, weights, "weights", (n_tok, top_k), _F32, dev), n_tok, top_k, d,
+            _arg(call, dYs, "dYs", shape, dY.dtype, dev),
+            _arg(call, dweights, "dweights", (n_tok, top_k), _F32, dev))

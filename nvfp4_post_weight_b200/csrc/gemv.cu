@@ -36,6 +36,7 @@ struct Args {
   Product p;
   int slice;            // chunks of K per CTA of the cluster
   int stage;            // chunks of tokens in shared memory at a time
+  int* status;          // the call's status word, or null: cleared (no wait here can run out)
 };
 
 // Eight codes (one word) as four bf16 pairs: elements (0,4), (1,5), (2,6),
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
 
   const Product& a = args.p;
+  if (args.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *args.status = 0;
   int e, first, count;
   if (!find_pass(a, (int)a.n_rows, blockIdx.y, &e, &first, &count))
     return;   // (the whole cluster: it shares blockIdx.y)
@@ -331,9 +333,10 @@ nvfp4_status launch_kernel(const Args& a, dim3 grid, int S, size_t smem, cudaStr
   return NVFP4_OK;
 }
 
-nvfp4_status launch_general(const Product& p, cudaStream_t st) {
+nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
   Args a{};
   a.p = p;
+  a.status = status;
   const bool glu = p.n_w == 2;
   const int64_t tiles = (p.d_out + kRowsCta - 1) / kRowsCta;
   const int64_t slots = !p.offsets ? 1 : p.n_experts < p.n_rows ? p.n_experts : p.n_rows;
@@ -383,6 +386,20 @@ nvfp4_status launch_general(const Product& p, cudaStream_t st) {
 #undef NVFP4_PRODUCT_W
   if (s == NVFP4_OK) count_launches(1);
   return s;
+}
+
+// Whether the FP4 path is the faster one.  Its CTAs walk all of K one after
+// another (some 0.25 us per 256 columns) however few rows they have, where this
+// kernel also slices K; measured, us, FP4 / this kernel, one token and 32:
+// 1024 x 8192: 14.7 / 8.8 and 24.6 / 16.6; 8192 x 8192: 17.2 / 20.9 and 26.2 /
+// 40.9; 8192 x 2048: 8.6 / 8.8 and 13.3 / 15.9; 1024 x 512: 6.7 / 7.1 and 10.3 /
+// 14.5.  By expert, where the rows first have to be found: 8 experts of 256 x
+// 512, 8 rows: 11.6 / 8.6; 32 of 768 x 2048, 32 rows: 16.0 / 15.8, 128 rows: 20.5
+// / 27.4.
+bool product_fp4_pays(const Product& p) {
+  const int64_t slots = p.n_experts < p.n_rows ? p.n_experts : p.n_rows;
+  if (p.offsets) return p.d_out * slots >= 24576;
+  return p.d_out >= 6144 || p.d_in <= 1024;
 }
 
 constexpr int64_t kMaxDim = 1 << 17, kMaxRows = 1 << 22;
@@ -439,9 +456,9 @@ nvfp4_status product(const void* X, nvfp4_dtype xt, int64_t n_x, const int* rows
   p.y_bf16 = yt == NVFP4_BF16;
   cudaStream_t st = as_cuda(stream);
   ProfileScope ps(kPhaseProduct, st);
-  if (need && product_fp4_supported(p)) return launch_product_fp4(p, ws, st);
-  if (need) NVFP4_CUDA_TRY(cudaMemsetAsync(ws, 0, sizeof(int), st));   // the status word
-  return launch_general(p, st);
+  if (need && product_fp4_supported(p) && product_fp4_pays(p))
+    return launch_product_fp4(p, ws, st);
+  return launch_general(p, need ? static_cast<int*>(ws) : nullptr, st);
 }
 
 }  // namespace

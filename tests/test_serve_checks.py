@@ -165,12 +165,51 @@ def test_binding_refuses_wrong_shapes_types_and_streams():
             print(k)
 
 
+class _On:
+    """A tensor as the binding's checks see it, on a device of any number."""
+    is_cuda, dtype, shape = True, torch.float32, (2,)
+
+    def __init__(self, n):
+        self.n, self.device = n, torch.device("cuda", n)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.n
+
+    def data_ptr(self):
+        return 256
+
+
 def test_a_stream_or_tensor_of_another_device_is_refused(monkeypatch):
-    """The device check comes before the library is called."""
-    class T:
-        def __init__(self, dev):
-            self.device = torch.device(dev)
-    with pytest.raises(B.Nvfp4Error, match="tensors on"):
-        B._run_on("nvfp4_gemv", [T("cuda:0"), T("cuda:1")], None)
-    with pytest.raises(B.Nvfp4Error, match="stream of"):
-        B._run_on("nvfp4_gemv", [T("cuda:1")], T("cuda:0"))
+    """The device checks come before the library is called; the call itself runs
+    with the tensors' device current."""
+    monkeypatch.setattr(torch, "Tensor", _On)
+    assert B._arg("nvfp4_gemv", _On(1), "Y", (2,), torch.float32, 1) == 256
+    with pytest.raises(B.Nvfp4Error, match="tensors on cuda:0 and cuda:1"):
+        B._arg("nvfp4_gemv", _On(1), "Y", (2,), torch.float32, 0)
+    stream = type("S", (), dict(device=torch.device("cuda", 0), cuda_stream=7))()
+    with pytest.raises(B.Nvfp4Error, match="stream of cuda:0, tensors on cuda:1"):
+        B._run_on("nvfp4_gemv", 1, stream)
+    seen = []
+
+    class device:
+        def __init__(self, n):
+            self.n = n
+
+        def __enter__(self):
+            seen.append(self.n)
+
+        def __exit__(self, *a):
+            seen.append("out")
+
+    class L:
+        def nvfp4_gemv(self, *a):
+            seen.append(a)
+            return 0
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(B, "lib", L)
+    B._run_on("nvfp4_gemv", 0, stream, 5)
+    assert seen == [0, (5, 7), "out"]
