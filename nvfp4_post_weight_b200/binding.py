@@ -118,7 +118,7 @@ def _load(path):
                                vp], i32),
         "nvfp4_layer_error_workspace_size": ([i64, i64], sz),
         "nvfp4_layer_error": ([vp, i32, vp, vp, vp, vp, i64, i64, vp, vp, sz, vp], i32),
-        "nvfp4_gemv_workspace_size": ([i64, i64], sz),
+        "nvfp4_gemv_workspace_size": ([i64, i64, i64, i64], sz),
         "nvfp4_gemv": ([vp, i32, i64, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp], i32),
         "nvfp4_gemv_swiglu": ([vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp],
                               i32),
@@ -630,6 +630,11 @@ def nvfp4_layer_error_batched(Ws, codes, scales, global_scales, Hs, errs, ws, st
 # ---------------------------------------------------------------------------
 # products with the solved weights, and tokens by expert and back
 # ---------------------------------------------------------------------------
+# the current stream's handle without a Stream object around it
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 # (these calls may take a few microseconds on the device, so their checks first
 # ask what holds for good arguments and leave the message to _need)
 def _arg(call, t, name, shape, dtype, dev):
@@ -662,7 +667,7 @@ def _run_on(call, dev, stream, *args):
     """Calls the library on the given stream of device number dev (None: its
     current one), with that device current."""
     if stream is None:
-        raw = torch.cuda.current_stream(dev).cuda_stream
+        raw = _current_raw_stream(dev)
     elif stream.device.index == dev:
         raw = stream.cuda_stream
     else:
@@ -690,9 +695,10 @@ def _weight(call, name, w, lead, d_out, d_in, dev):
 
 
 @functools.lru_cache(maxsize=1024)
-def nvfp4_gemv_workspace_size(n_rows, d_in) -> int:
-    """Workspace bytes of a product with n_rows rows of Y and d_in columns of X."""
-    return int(lib().nvfp4_gemv_workspace_size(int(n_rows), int(d_in)))
+def nvfp4_gemv_workspace_size(n_rows, d_out, d_in, n_experts=0) -> int:
+    """Workspace bytes of a product with n_rows rows of Y by a d_out x d_in
+    matrix (or pair), or by n_experts of them."""
+    return int(lib().nvfp4_gemv_workspace_size(int(n_rows), int(d_out), int(d_in), int(n_experts)))
 
 
 def _product(call, X, weights, Y, offsets, rows, ws, stream):
@@ -716,7 +722,7 @@ def _product(call, X, weights, Y, offsets, rows, ws, stream):
     w = []
     for name, t in weights:
         w += _weight(call, name, t, lead, d_out, d_in, dev)
-    nws = nvfp4_gemv_workspace_size(n_rows, d_in)
+    nws = nvfp4_gemv_workspace_size(n_rows, d_out, d_in, lead[0] if lead else 0)
     if ws is not None:
         _ws_bytes(call, ws, nws)
         pws, nws = _arg(call, ws, "workspace", ws.shape, _U8, dev), ws.numel()
@@ -732,7 +738,7 @@ def _product(call, X, weights, Y, offsets, rows, ws, stream):
 
 def nvfp4_gemv(X, codes, scales, global_scale, Y, ws=None, stream=None):
     """Y (n_tok x d_out) = X (n_tok x d_in) Q^T from the codes as solved; X and
-    Y each bf16 or fp32.  ws: nvfp4_gemv_workspace_size(n_tok, d_in) bytes
+    Y each bf16 or fp32.  ws: nvfp4_gemv_workspace_size bytes
     (here and below; torch's allocator provides them otherwise)."""
     _product("nvfp4_gemv", X, [("", (codes, scales, global_scale))], Y, None, None, ws, stream)
 

@@ -396,10 +396,11 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
 // 14.5.  By expert, where the rows first have to be found: 8 experts of 256 x
 // 512, 8 rows: 11.6 / 8.6; 32 of 768 x 2048, 32 rows: 16.0 / 15.8, 128 rows: 20.5
 // / 27.4.
-bool product_fp4_pays(const Product& p) {
-  const int64_t slots = p.n_experts < p.n_rows ? p.n_experts : p.n_rows;
-  if (p.offsets) return p.d_out * slots >= 24576;
-  return p.d_out >= 6144 || p.d_in <= 1024;
+// Sizes only: they decide the workspace too.  n_experts 0: one matrix.
+bool fp4_path(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts) {
+  if (!product_fp4_shape(n_rows, d_in)) return false;
+  if (n_experts > 0) return d_out * (n_experts < n_rows ? n_experts : n_rows) >= 24576;
+  return d_out >= 6144 || d_in <= 1024;
 }
 
 constexpr int64_t kMaxDim = 1 << 17, kMaxRows = 1 << 22;
@@ -438,7 +439,8 @@ nvfp4_status product(const void* X, nvfp4_dtype xt, int64_t n_x, const int* rows
   if (!is_aligned(X, 16) || !is_aligned(Y, yt == NVFP4_BF16 ? 2 : 4) || !is_aligned(rows, 4) ||
       !is_aligned(offsets, 4))
     return NVFP4_ERR_INVALID_ARG;
-  const size_t need = any && product_fp4_shape(n_rows, d_in) ? product_fp4_ws_bytes(n_rows, d_in) : 0;
+  const bool fp4 = any && fp4_path(n_rows, d_out, d_in, offsets ? n_experts : 0);
+  const size_t need = fp4 ? product_fp4_ws_bytes(n_rows, d_in) : 0;
   if (need && (!ws || !is_aligned(ws, 256) || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (!any) return NVFP4_OK;
   p.X = X;
@@ -456,8 +458,7 @@ nvfp4_status product(const void* X, nvfp4_dtype xt, int64_t n_x, const int* rows
   p.y_bf16 = yt == NVFP4_BF16;
   cudaStream_t st = as_cuda(stream);
   ProfileScope ps(kPhaseProduct, st);
-  if (need && product_fp4_supported(p) && product_fp4_pays(p))
-    return launch_product_fp4(p, ws, st);
+  if (fp4 && product_fp4_supported(p)) return launch_product_fp4(p, ws, st);
   return launch_general(p, need ? static_cast<int*>(ws) : nullptr, st);
 }
 
@@ -468,8 +469,8 @@ using namespace nvfp4;
 
 extern "C" {
 
-size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_in) {
-  if (!product_fp4_shape(n_rows, d_in)) return 0;
+size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts) {
+  if (n_rows < 0 || d_out < 0 || n_experts < 0 || !fp4_path(n_rows, d_out, d_in, n_experts)) return 0;
   return product_fp4_ws_bytes(n_rows, d_in);
 }
 
