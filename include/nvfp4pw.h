@@ -473,8 +473,8 @@ nvfp4_status nvfp4_dequant_batched(int count, const uint8_t* const* codes,
  *           quantize call.
  * Y       : n_tok x d_out, bf16 or fp32 (y_dtype, its own choice), fully
  *           written; must not overlap X.  d_in == 0 gives zeros.
- * ws      : workspace of nvfp4_gemv_workspace_size(n_tok, d_out, d_in, 0) bytes,
- *           256-byte aligned (0 for sizes that need none; NULL is then fine).  Its first
+ * ws      : workspace of nvfp4_gemv_workspace_size(n_tok, d_out, d_in, 0, 0)
+ *           bytes, 256-byte aligned (0 for sizes that need none; NULL is then fine).  Its first
  *           int is the status word (nvfp4_workspace_status): a timed-out wait
  *           sets NVFP4_ERR_TIMEOUT, Y is then unspecified.
  * The products are exact, their sums fp32, and Y is rounded once.  Sizes that
@@ -494,9 +494,10 @@ nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const
                         size_t ws_bytes, nvfp4_stream_t stream);
 
 /* Bytes of workspace of the products: n_rows rows of Y (n_tok, or the experts
- * forms' n_rows), the matrices' sizes, and the experts forms' n_experts (0 for
- * the forms with one matrix or pair). */
-size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts);
+ * forms' n_rows), the matrices' sizes, the experts forms' n_experts (0 for the
+ * others), pair: 1 for the swiglu forms. */
+size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts,
+                                 int pair);
 
 /* The gated pair of a feed-forward layer in one pass:
  *   Y = silu(X Qg^T) * (X Qu^T),  silu(g) = g / (1 + exp(-g)),

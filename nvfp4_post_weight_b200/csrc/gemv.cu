@@ -341,9 +341,9 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
   const int64_t tiles = (p.d_out + kRowsCta - 1) / kRowsCta;
   const int64_t slots = !p.offsets ? 1 : p.n_experts < p.n_rows ? p.n_experts : p.n_rows;
   const int n_chunks = (int)((p.d_in + kChunk - 1) / kChunk);
-  // slices of K: until the CTAs fill the GPU four times, each of four chunks at least
+  // slices of K: until the CTAs fill the GPU (two an SM), each of two chunks at least
   int S = 1;
-  while (S < 8 && tiles * slots * S < 4 * num_sms() && n_chunks >= 8 * S) S *= 2;
+  while (S < 8 && tiles * slots * S < 2 * num_sms() && n_chunks >= 4 * S) S *= 2;
   a.slice = (n_chunks + S - 1) / S;
   // tokens per pass: the rows of one expert on average
   const int64_t mean = (p.n_rows + slots - 1) / slots;
@@ -391,15 +391,19 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
 // Whether the FP4 path is the faster one.  Its CTAs walk all of K one after
 // another (some 0.25 us per 256 columns) however few rows they have, where this
 // kernel also slices K; measured, us, FP4 / this kernel, one token and 32:
-// 1024 x 8192: 14.7 / 8.8 and 24.6 / 16.6; 8192 x 8192: 17.2 / 20.9 and 26.2 /
+// 1024 x 8192: 14.7 / 6.5 and 24.6 / 16.6; 8192 x 8192: 17.2 / 20.9 and 26.2 /
 // 40.9; 8192 x 2048: 8.6 / 8.8 and 13.3 / 15.9; 1024 x 512: 6.7 / 7.1 and 10.3 /
-// 14.5.  By expert, where the rows first have to be found: 8 experts of 256 x
-// 512, 8 rows: 11.6 / 8.6; 32 of 768 x 2048, 32 rows: 16.0 / 15.8, 128 rows: 20.5
-// / 27.4.
-// Sizes only: they decide the workspace too.  n_experts 0: one matrix.
-bool fp4_path(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts) {
+// 14.5.  By expert it also has to find its rows, so the bytes of the experts'
+// codes decide, the more rows they have the sooner: 32 experts of 768 x 2048
+// (25 MB), one row each 13.3 / 11.0, four 20.5 / 25.0; 8 pairs of 1536 x 4096
+// (50 MB), one row each 20.2 / 25.2.  Sizes only: they decide the workspace too.
+// n_experts 0: one matrix or pair.
+bool fp4_path(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, int n_w) {
   if (!product_fp4_shape(n_rows, d_in)) return false;
-  if (n_experts > 0) return d_out * (n_experts < n_rows ? n_experts : n_rows) >= 24576;
+  if (n_experts > 0) {
+    const int64_t slots = n_experts < n_rows ? n_experts : n_rows, mean = n_rows / slots;
+    return n_w * slots * d_out * d_in / 2 * (mean < 4 ? mean : 4) >= 48000000;
+  }
   return d_out >= 6144 || d_in <= 1024;
 }
 
@@ -439,7 +443,7 @@ nvfp4_status product(const void* X, nvfp4_dtype xt, int64_t n_x, const int* rows
   if (!is_aligned(X, 16) || !is_aligned(Y, yt == NVFP4_BF16 ? 2 : 4) || !is_aligned(rows, 4) ||
       !is_aligned(offsets, 4))
     return NVFP4_ERR_INVALID_ARG;
-  const bool fp4 = any && fp4_path(n_rows, d_out, d_in, offsets ? n_experts : 0);
+  const bool fp4 = any && fp4_path(n_rows, d_out, d_in, offsets ? n_experts : 0, n_w);
   const size_t need = fp4 ? product_fp4_ws_bytes(n_rows, d_in) : 0;
   if (need && (!ws || !is_aligned(ws, 256) || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (!any) return NVFP4_OK;
@@ -469,8 +473,11 @@ using namespace nvfp4;
 
 extern "C" {
 
-size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts) {
-  if (n_rows < 0 || d_out < 0 || n_experts < 0 || !fp4_path(n_rows, d_out, d_in, n_experts)) return 0;
+size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts,
+                                 int pair) {
+  if (n_rows < 0 || d_out < 0 || n_experts < 0 ||
+      !fp4_path(n_rows, d_out, d_in, n_experts, pair ? 2 : 1))
+    return 0;
   return product_fp4_ws_bytes(n_rows, d_in);
 }
 

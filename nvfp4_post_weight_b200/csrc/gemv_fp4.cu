@@ -272,9 +272,17 @@ struct Pieces {
   int64_t u, u_end, units;
   __device__ __forceinline__ void init(const Fp4Args& a) {
     units = (a.p.d_out + kUnit - 1) / kUnit;
-    const int64_t all = count_passes(a.p, a.tokens) * units;
-    u = all * blockIdx.x / gridDim.x;
-    u_end = all * (blockIdx.x + 1) / gridDim.x;
+    const int passes = count_passes(a.p, a.tokens), ctas = gridDim.x, b = blockIdx.x;
+    const int per = passes ? ctas / passes : 0;   // CTAs per pass
+    if (per * passes * 16 >= ctas * 15) {
+      // few passes: a whole number of CTAs each, so that no CTA has two pieces
+      u = b < per * passes ? b / per * units + units * (b % per) / per : 0;
+      u_end = b < per * passes ? b / per * units + units * (b % per + 1) / per : 0;
+    } else {
+      const int64_t all = passes * units;
+      u = all * b / ctas;
+      u_end = all * (b + 1) / ctas;
+    }
   }
   // Warp-wide.
   __device__ __forceinline__ bool next(const Fp4Args& a, Piece* q) {

@@ -335,3 +335,202 @@ def test_a_solved_decoder_layer_answers():
     y = s.linear("down", h, stream=side)
     side.synchronize()
     close(y, *sums(h, s.weight("down")))
+
+
+# ---- the block-scaled FP4 tensor-core path ---------------------------------------
+def fp4(n_rows, d_out, d_in, n_experts=0, pair=False):
+    """Whether these sizes run there."""
+    return B.nvfp4_gemv_workspace_size(n_rows, d_out, d_in, n_experts, pair) > 0
+
+
+def sums_fp4(x, w):
+    """sums() with what the digits leave out of a token: 2^-22 of the largest of
+    each block of 16 entries, or 2^-39 of the token's largest."""
+    x64 = x.double()
+    top = x64.abs().unflatten(1, (-1, 16)).amax(2)
+    left = torch.maximum(top * 2.0 ** -22, x64.abs().amax(1, keepdim=True) * 2.0 ** -39)
+    q = dequantised(*w)
+    y, tol = sums(x, w)
+    return y, tol + left.repeat_interleave(16, 1) @ q.abs().T
+
+
+def gated_fp4(x, gate, up):
+    (g, dg), (u, du) = sums_fp4(x, gate), sums_fp4(x, up)
+    s = g * torch.sigmoid(g)
+    return s * u, 1.1 * u.abs() * dg + s.abs() * du + 1.1 * dg * du + \
+        8 * 2.0 ** -23 * (s * u).abs() + 1e-36
+
+
+@pytest.mark.parametrize("n_tok", [1, 2, 7, 8, 16, 17, 24, 25, 32, 33, 70])
+@pytest.mark.parametrize("d_out,d_in", [(6144, 2048), (7001, 512), (30000, 256), (40, 768), (8, 256)])
+def test_gemv_fp4(n_tok, d_out, d_in):
+    """One and several passes over the tokens, one and several tiles a CTA, rows
+    that end inside a unit, one panel and several."""
+    assert fp4(n_tok, d_out, d_in)
+    w = weights((d_out, d_in), d_out + d_in)
+    for xt, yt in ((BF16, F32), (F32, BF16), (BF16, BF16), (F32, F32)):
+        x = acts(n_tok, d_in, xt, n_tok)
+        y = torch.full((n_tok, d_out), 7.0, dtype=yt, device=DEV)
+        B.nvfp4_gemv(x, *w, y)
+        close(y, *sums_fp4(x, w))
+
+
+@pytest.mark.parametrize("n_tok", [1, 5, 24, 25, 49])
+@pytest.mark.parametrize("d_out,d_in", [(6144, 1024), (20011, 256), (100, 512)])
+def test_gemv_swiglu_fp4(n_tok, d_out, d_in):
+    assert fp4(n_tok, d_out, d_in, 0, True)
+    gate, up = weights((d_out, d_in), 1 + d_in), weights((d_out, d_in), 2 + d_in)
+    for xt in (BF16, F32):
+        x = acts(n_tok, d_in, xt, n_tok) * 0.1
+        y = torch.full((n_tok, d_out), 7.0, dtype=xt, device=DEV)
+        B.nvfp4_gemv_swiglu(x, gate, up, y)
+        close(y, *gated_fp4(x, gate, up))
+
+
+def test_fp4_bf16_entries_near_their_block_are_exact():
+    """Entries within 2^-14 of their block's largest lose nothing: one nonzero
+    weight a column picks single entries out exactly."""
+    d_in = d_out = 256
+    assert fp4(4, d_out, d_in)
+    g = torch.Generator().manual_seed(1)
+    x = (torch.rand((4, d_in), generator=g) + 1) * 2.0 ** -torch.randint(0, 14, (4, d_in), generator=g)
+    x = (x * (torch.randint(0, 2, (4, d_in), generator=g) * 2 - 1)).to(BF16).to(DEV)
+    x[:, ::16] = 1.5   # (the largest lies in [1, 2) of every block)
+    codes = torch.zeros((d_out, d_in), dtype=torch.uint8)
+    codes[torch.arange(d_out), torch.arange(d_in)] = 2          # 1.0
+    packed = (codes[:, 0::2] | codes[:, 1::2] << 4).to(DEV)
+    scales = torch.full((d_out, d_in // 16), 56, dtype=torch.uint8, device=DEV)   # 1.0
+    y = torch.empty((4, d_out), device=DEV)
+    B.nvfp4_gemv(x, packed, scales, torch.ones(1, device=DEV), y)
+    assert torch.equal(y, x.float())
+
+
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_fp4_extreme_and_nonfinite_tokens(xt):
+    d_in, d_out = 512, 6200
+    w = weights((d_out, d_in), 3)
+    x = acts(9, d_in, F32, 4)
+    x[1] *= 1e30
+    x[2] *= 1e-30
+    x[3, :256] *= 1e-9            # blocks far below the token's largest
+    x[4] = 0
+    x = x.to(xt)
+    x[5, 3], x[6, 400], x[6, 9] = float("nan"), float("inf"), 1.0
+    x[7] = 2.0 ** -126
+    y = torch.empty((9, d_out), device=DEV)
+    B.nvfp4_gemv(x, *w, y)
+    keep = [0, 1, 2, 3, 4, 7, 8]
+    ref, tol = sums_fp4(x[keep], w)
+    assert ((y[keep].double() - ref).abs() <= tol + 2.0 ** -23 * ref.abs() + 2.0 ** -148).all()
+    bad = (x[5:7].double()[:, None, :] * dequantised(*w)[None]).sum(-1)
+    assert torch.equal(torch.isnan(y[5:7]), torch.isnan(bad))
+    inf = torch.isinf(bad)
+    assert inf.any() and torch.equal(y[5:7][inf].double(), bad[inf])
+
+
+FP4_COUNTS = [[1] * 40, [0, 16, 0, 17, 0, 0, 33, 1] * 5, [200], [3, 0, 5, 1, 1, 2, 0, 4] * 16]
+
+
+@pytest.mark.parametrize("counts", FP4_COUNTS)
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("xt", [BF16, F32])
+def test_experts_fp4(counts, pair, xt):
+    """Pieces of several experts a CTA and several CTAs an expert, more rows than
+    a pass holds, rows behind the last expert's left as they were."""
+    E, n, d_in = len(counts), sum(counts), 512
+    d_out = max(200, -(-48000000 // (min(E, n) * d_in // 2)) // 8 * 8 + 13)
+    n_rows = n + 3
+    assert fp4(n_rows, d_out, d_in, E, pair)
+    ws_ = [weights((E, d_out, d_in), s) for s in ((5, 6) if pair else (5,))]
+    x = acts(50, d_in, xt, 9) * 0.1
+    rows = torch.randint(0, 50, (n_rows,), dtype=torch.int32, device=DEV)
+    rows[0], rows[n // 2] = -1, 50    # read as rows of zeros
+    offsets = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
+    y = torch.full((n_rows, d_out), 7.0, dtype=xt, device=DEV)
+    if pair:
+        B.nvfp4_gemv_swiglu_experts(x, offsets, ws_[0], ws_[1], y, rows)
+    else:
+        B.nvfp4_gemv_experts(x, offsets, *ws_[0], y, rows)
+    bad = (rows < 0) | (rows >= 50)
+    xr = torch.where(bad[:, None], torch.zeros((), dtype=xt, device=DEV),
+                     x[rows.clamp(0, 49).long()])
+    fn = gated_fp4 if pair else sums_fp4
+    by_expert(lambda r, *m: close(y[r], *fn(xr[r], *m)), offsets, *ws_)
+    assert (y[n:] == 7).all()
+
+
+def test_fp4_bad_offsets_are_cut():
+    E, d_in = 3, 1024
+    d_out = 40000
+    assert fp4(4, d_out, d_in, E)
+    w, x = weights((E, d_out, d_in), 1), acts(4, d_in, BF16, 1)
+    y = torch.full((4, d_out), 7.0, device=DEV)
+    for offsets, mine in (([-5, 2, 2, 99], {0: 0, 1: 0, 2: 2, 3: 2}), ([3, 1, 2, 2], {1: 1}),
+                          ([0, 0, 0, 0], {})):
+        y.fill_(7)
+        B.nvfp4_gemv_experts(x, torch.tensor(offsets, dtype=torch.int32, device=DEV), *w, y)
+        for r in range(4):
+            if r in mine:
+                e = mine[r]
+                close(y[r:r + 1], *sums_fp4(x[r:r + 1], (w[0][e], w[1][e], w[2][e])))
+            else:
+                assert (y[r] == 7).all()
+
+
+def test_fp4_unaligned_bases_run_elsewhere():
+    """Codes 8 bytes or scales one byte off a 16-byte boundary: same answer."""
+    d_out, d_in = 300, 512
+    w, x = weights((d_out, d_in), 8), acts(3, d_in, BF16, 2)
+    codes = torch.empty(w[0].numel() + 8, dtype=torch.uint8, device=DEV)[8:].view(w[0].shape)
+    scales = torch.empty(w[1].numel() + 1, dtype=torch.uint8, device=DEV)[1:].view(w[1].shape)
+    codes.copy_(w[0])
+    scales.copy_(w[1])
+    for c, s in ((codes, w[1]), (w[0], scales), (w[0], w[1])):
+        ws = B.workspace(B.nvfp4_gemv_workspace_size(3, d_out, d_in), DEV)
+        ws[:4] = 255
+        y = torch.empty((3, d_out), device=DEV)
+        B.nvfp4_gemv(x, c, s, w[2], y, ws)
+        close(y, *sums_fp4(x, w))
+        assert B.nvfp4_workspace_status(ws) == 0
+
+
+def test_fp4_same_bits_on_streams_and_in_graphs():
+    d_out, d_in = 6500, 1024
+    w, x = weights((d_out, d_in), 31), acts(6, d_in, BF16, 3)
+    y, z, v = (torch.empty((6, d_out), device=DEV) for _ in range(3))
+    ws = [B.workspace(B.nvfp4_gemv_workspace_size(6, d_out, d_in), DEV) for _ in range(2)]
+    B.nvfp4_gemv(x, *w, y, ws[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.nvfp4_gemv(x, *w, z, ws[0])
+        B.nvfp4_gemv(x, *w, z)            # a workspace from the graph's pool
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    z.zero_()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        graph.replay()
+        B.nvfp4_gemv(x, *w, v, ws[1], stream=side)
+        B.nvfp4_gemv(x, *w, v, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y, z) and torch.equal(y, v)
+
+
+def test_fp4_timeout_is_reported_and_the_context_survives():
+    """With a wait limit of 1 ns every wait of the kernel gives up: the status
+    says so, and the next call is right again."""
+    d_out, d_in = 7000, 1024
+    w, x = weights((d_out, d_in), 5), acts(5, d_in, BF16, 3)
+    y = torch.zeros((5, d_out), device=DEV)
+    ws = B.workspace(B.nvfp4_gemv_workspace_size(5, d_out, d_in), DEV)
+    torch.cuda.synchronize()
+    B.nvfp4_set_wait_limit_ns(1)
+    try:
+        B.nvfp4_gemv(x, *w, y, ws)
+        torch.cuda.synchronize()
+    finally:
+        B.nvfp4_set_wait_limit_ns(0)
+    assert B.nvfp4_workspace_status(ws) == 6
+    B.nvfp4_gemv(x, *w, y, ws)
+    assert B.nvfp4_workspace_status(ws) == 0
+    close(y, *sums_fp4(x, w))
