@@ -473,15 +473,16 @@ nvfp4_status nvfp4_dequant_batched(int count, const uint8_t* const* codes,
  *           quantize call.
  * Y       : n_tok x d_out, bf16 or fp32 (y_dtype, its own choice), fully
  *           written; must not overlap X.  d_in == 0 gives zeros.
- * ws      : workspace of nvfp4_gemv_workspace_size(n_tok, d_out, d_in, 0, 0)
- *           bytes, 256-byte aligned (0 for sizes that need none; NULL is then fine).  Its first
+ * ws      : workspace of nvfp4_gemv_workspace_size(n_tok, d_out, d_in, 0,
+ *           0, x_dtype) bytes, 256-byte aligned (0 for calls that need none, NULL is
+ *           then fine).  Its first
  *           int is the status word (nvfp4_workspace_status): a timed-out wait
  *           sets NVFP4_ERR_TIMEOUT, Y is then unspecified.
- * The products are exact, their sums fp32, and Y is rounded once.  Sizes that
+ * The products are exact, their sums fp32, and Y is rounded once.  Calls that
  * need a workspace run on the block-scaled FP4 tensor cores where codes and
- * scales are 16-byte aligned: there a token's entry is kept to 2^-22 of
+ * scales are 16-byte aligned: there a (bf16) token's entry is kept to 2^-22 of
  * the largest of its block of 16 columns, or to 2^-39 of the token's largest
- * where that is more (bf16 entries within 2^-14 of their block's largest are
+ * where that is more (entries within 2^-14 of their block's largest are
  * exact); elsewhere tokens are used at all their bits.  NaN and infinite
  * tokens behave as in the plain product and stay in their row, and scale code
  * 127 (a NaN, which the quantize call does not write) may give any value in
@@ -495,9 +496,9 @@ nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const
 
 /* Bytes of workspace of the products: n_rows rows of Y (n_tok, or the experts
  * forms' n_rows), the matrices' sizes, the experts forms' n_experts (0 for the
- * others), pair: 1 for the swiglu forms. */
+ * others), pair: 1 for the swiglu forms, X's type. */
 size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts,
-                                 int pair);
+                                 int pair, nvfp4_dtype x_dtype);
 
 /* The gated pair of a feed-forward layer in one pass:
  *   Y = silu(X Qg^T) * (X Qu^T),  silu(g) = g / (1 + exp(-g)),

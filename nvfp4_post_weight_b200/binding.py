@@ -118,7 +118,7 @@ def _load(path):
                                vp], i32),
         "nvfp4_layer_error_workspace_size": ([i64, i64], sz),
         "nvfp4_layer_error": ([vp, i32, vp, vp, vp, vp, i64, i64, vp, vp, sz, vp], i32),
-        "nvfp4_gemv_workspace_size": ([i64, i64, i64, i64, i32], sz),
+        "nvfp4_gemv_workspace_size": ([i64, i64, i64, i64, i32, i32], sz),
         "nvfp4_gemv": ([vp, i32, i64, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp], i32),
         "nvfp4_gemv_swiglu": ([vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp],
                               i32),
@@ -695,11 +695,13 @@ def _weight(call, name, w, lead, d_out, d_in, dev):
 
 
 @functools.lru_cache(maxsize=1024)
-def nvfp4_gemv_workspace_size(n_rows, d_out, d_in, n_experts=0, pair=False) -> int:
+def nvfp4_gemv_workspace_size(n_rows, d_out, d_in, n_experts=0, pair=False,
+                              dtype=torch.bfloat16) -> int:
     """Workspace bytes of a product with n_rows rows of Y by a d_out x d_in
-    matrix, or by n_experts of them; pair: the swiglu forms."""
+    matrix, or by n_experts of them; pair: the swiglu forms; dtype: X's."""
+    code = NVFP4_BF16 if dtype == torch.bfloat16 else NVFP4_F32
     return int(lib().nvfp4_gemv_workspace_size(int(n_rows), int(d_out), int(d_in), int(n_experts),
-                                               int(pair)))
+                                               int(pair), code))
 
 
 def _product(call, X, weights, Y, offsets, rows, ws, stream):
@@ -723,7 +725,8 @@ def _product(call, X, weights, Y, offsets, rows, ws, stream):
     w = []
     for name, t in weights:
         w += _weight(call, name, t, lead, d_out, d_in, dev)
-    nws = nvfp4_gemv_workspace_size(n_rows, d_out, d_in, lead[0] if lead else 0, len(weights) == 2)
+    nws = nvfp4_gemv_workspace_size(n_rows, d_out, d_in, lead[0] if lead else 0, len(weights) == 2,
+                                    X.dtype)
     if ws is not None:
         _ws_bytes(call, ws, nws)
         pws, nws = _arg(call, ws, "workspace", ws.shape, _U8, dev), ws.numel()

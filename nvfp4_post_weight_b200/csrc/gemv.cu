@@ -163,8 +163,8 @@ __device__ __forceinline__ void stage_tokens(const Product& a, int64_t t0, int n
 // columns, and experts.
 template <typename TX, int NW, int NT, bool kWide>
 __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const Args args) {
-  constexpr int kPlanes = sizeof(TX) == 2 ? 1 : 3;
-  constexpr int kDepth = NW == 1 ? 4 : 2;   // chunks loaded ahead
+  constexpr int kPlanes = sizeof(TX) == 2 ? 1 : 3, kAcc = kPlanes == 1 ? 2 : 3;
+  constexpr int kDepth = NW == 1 && kPlanes == 1 ? 4 : 2;   // chunks loaded ahead
   extern __shared__ uint4 smem[];
   cg::cluster_group cluster = cg::this_cluster();
   const int S = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
         for (int d = 0; d < kDepth; ++d) {
           const int c = cb + d;
           if (c >= c1) break;
-          float acc[NW][NT][4] = {};
+          float acc[NW][NT][kAcc][4] = {};
           uint32_t sc[NW][2][2];
 #pragma unroll
           for (int m = 0; m < NW; ++m)
@@ -255,20 +255,26 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
                   b = xs[pl * plane + ((c - c0) * n + tok) * 16 + ((4 * w + t) ^ ((tok & 1) << 2))];
 #pragma unroll
                 for (int m = 0; m < NW; ++m) {
-                  mma(acc[m][nt], A[m][0], b.x, b.y);
-                  mma(acc[m][nt], A[m][1], b.z, b.w);
+                  float* sum = acc[m][nt][pl == 0 ? w >> 1 : 2];
+                  mma(sum, A[m][0], b.x, b.y);
+                  mma(sum, A[m][1], b.z, b.w);
                 }
               }
             }
           }
-          // The matrix unit does not round its sums to nearest; a chunk's sum
-          // goes to an fp32 total, so that its error does not grow with K.
+          // The matrix unit does not round its sums to nearest: it makes chains of
+          // four (and one of the fp32 tokens' lesser pieces), which fp32 additions
+          // join, so that its error neither shows nor grows with K.
 #pragma unroll
           for (int m = 0; m < NW; ++m)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) tot[m][nt][i] += acc[m][nt][i];
+              for (int i = 0; i < 4; ++i) {
+                float sum = acc[m][nt][0][i] + acc[m][nt][1][i];
+                if (kAcc == 3) sum += acc[m][nt][kAcc - 1][i];
+                tot[m][nt][i] += sum;
+              }
           const int next = c + kDepth;
 #pragma unroll
           for (int m = 0; m < NW; ++m)
@@ -396,10 +402,11 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
 // 14.5.  By expert it also has to find its rows, so the bytes of the experts'
 // codes decide, the more rows they have the sooner: 32 experts of 768 x 2048
 // (25 MB), one row each 13.3 / 11.0, four 20.5 / 25.0; 8 pairs of 1536 x 4096
-// (50 MB), one row each 20.2 / 25.2.  Sizes only: they decide the workspace too.
+// (50 MB), one row each 20.2 / 25.2.  No addresses: the workspace goes by it too.
 // n_experts 0: one matrix or pair.
-bool fp4_path(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, int n_w) {
-  if (!product_fp4_shape(n_rows, d_in)) return false;
+bool fp4_path(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, int n_w,
+              nvfp4_dtype xt) {
+  if (xt != NVFP4_BF16 || !product_fp4_shape(n_rows, d_in)) return false;
   if (n_experts > 0) {
     const int64_t slots = n_experts < n_rows ? n_experts : n_rows, mean = n_rows / slots;
     return n_w * slots * d_out * d_in / 2 * (mean < 4 ? mean : 4) >= 48000000;
@@ -443,7 +450,7 @@ nvfp4_status product(const void* X, nvfp4_dtype xt, int64_t n_x, const int* rows
   if (!is_aligned(X, 16) || !is_aligned(Y, yt == NVFP4_BF16 ? 2 : 4) || !is_aligned(rows, 4) ||
       !is_aligned(offsets, 4))
     return NVFP4_ERR_INVALID_ARG;
-  const bool fp4 = any && fp4_path(n_rows, d_out, d_in, offsets ? n_experts : 0, n_w);
+  const bool fp4 = any && fp4_path(n_rows, d_out, d_in, offsets ? n_experts : 0, n_w, xt);
   const size_t need = fp4 ? product_fp4_ws_bytes(n_rows, d_in) : 0;
   if (need && (!ws || !is_aligned(ws, 256) || ws_bytes < need)) return NVFP4_ERR_WORKSPACE;
   if (!any) return NVFP4_OK;
@@ -474,9 +481,9 @@ using namespace nvfp4;
 extern "C" {
 
 size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts,
-                                 int pair) {
+                                 int pair, nvfp4_dtype x_dtype) {
   if (n_rows < 0 || d_out < 0 || n_experts < 0 ||
-      !fp4_path(n_rows, d_out, d_in, n_experts, pair ? 2 : 1))
+      !fp4_path(n_rows, d_out, d_in, n_experts, pair ? 2 : 1, x_dtype))
     return 0;
   return product_fp4_ws_bytes(n_rows, d_in);
 }

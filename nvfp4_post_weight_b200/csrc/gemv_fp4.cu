@@ -1,4 +1,4 @@
-// Products of a few tokens with NVFP4 weights on the block-scaled FP4 tensor
+// Products of a few bf16 tokens with NVFP4 weights on the block-scaled FP4 tensor
 // cores: the codes and the block scales go to the matrix unit as they are
 // (tcgen05.mma kind::mxf4nvf4, 16-element blocks with E4M3 scales), and the
 // tokens are taken apart into FP4 digits instead.
@@ -11,7 +11,8 @@
 // x . q = 2^(E - 29) sum_p 8^p D_p.  The products are exact; a column is summed
 // in fp32 by the matrix unit.  An entry is kept to 2^-22 of the largest of its
 // block, or to 2^-39 of the token's largest (blocks more than 17 octaves below
-// it), so bf16 entries within 2^-14 of their block's largest are exact.
+// it), and bf16 entries within 2^-14 of their block's largest are exact.  (fp32
+// tokens would lose bits of every entry; they take the other kernel.)
 //
 // The weights' bytes bound the product: nothing is decoded, a warp's lanes issue
 // the copies and one thread the matrix instructions.  One CTA per SM streams
@@ -64,20 +65,13 @@ struct Fp4Args {
 // CTA (r, part): sorted row r (zeros if it points outside X), 4096 columns.
 constexpr int kDigitThreads = 512, kDigitCols = kDigitThreads * 8;
 
-template <typename TX>
-__device__ __forceinline__ void load8(const TX* p, float* f) {
-  if constexpr (sizeof(TX) == 2) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t h[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t h[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(h[j] << 16);
-      f[2 * j + 1] = __uint_as_float(h[j] & 0xFFFF0000u);
-    }
-  } else {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = __uint_as_float(h[j] << 16);
+    f[2 * j + 1] = __uint_as_float(h[j] & 0xFFFF0000u);
   }
 }
 
@@ -93,7 +87,6 @@ __device__ __forceinline__ int64_t x_row(const Product& p, int64_t r) {
   return x < p.n_x ? x : -1;
 }
 
-template <typename TX>
 __global__ void __launch_bounds__(kDigitThreads)
     digits_kernel(const Product p, uint8_t* __restrict__ digits,
                   uint8_t* __restrict__ sf, int* __restrict__ expo, int* status) {
@@ -102,7 +95,7 @@ __global__ void __launch_bounds__(kDigitThreads)
   const int64_t r = blockIdx.x;
   const int d_in = (int)p.d_in;
   const int64_t row = x_row(p, r);
-  const TX* x = static_cast<const TX*>(p.X) + row * d_in;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.X) + row * d_in;
   if (r == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
   // the row's largest magnitude (bits order like values; not finite: above all)
   uint32_t big = 0;
@@ -308,8 +301,7 @@ __device__ __noinline__ float plain_product(const Product& p, int w, int e, int6
     const float scale = (float)e4m3_value(p.scales[w][block + b] & 0x7F);
     for (int j = 0; j < kBlock; ++j) {
       const int64_t k = x * p.d_in + b * kBlock + j;
-      const float v = p.x_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.X)[k])
-                               : static_cast<const float*>(p.X)[k];
+      const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.X)[k]);
       sum = fmaf(v, e2m1_value((j < 8 ? c.x : c.y) >> (4 * (j & 7)) & 0xF) * scale, sum);
     }
   }
@@ -649,10 +641,7 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
   a.sf = sf;
   a.digits = digits;
   const dim3 grid((unsigned)p.n_rows, (unsigned)((p.d_in + kDigitCols - 1) / kDigitCols));
-  if (p.x_bf16)
-    digits_kernel<__nv_bfloat16><<<grid, kDigitThreads, 0, st>>>(p, digits, sf, expo, a.status);
-  else
-    digits_kernel<float><<<grid, kDigitThreads, 0, st>>>(p, digits, sf, expo, a.status);
+  digits_kernel<<<grid, kDigitThreads, 0, st>>>(p, digits, sf, expo, a.status);
   NVFP4_LAUNCH_CHECK();
   // tokens per pass: what the accumulators hold, in equal passes; for experts
   // 16, so that an expert's rows of a small batch take one pass

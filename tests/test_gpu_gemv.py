@@ -339,7 +339,7 @@ def test_a_solved_decoder_layer_answers():
 
 # ---- the block-scaled FP4 tensor-core path ---------------------------------------
 def fp4(n_rows, d_out, d_in, n_experts=0, pair=False):
-    """Whether these sizes run there."""
+    """Whether bf16 tokens of these sizes run there (fp32 ones do not)."""
     return B.nvfp4_gemv_workspace_size(n_rows, d_out, d_in, n_experts, pair) > 0
 
 
