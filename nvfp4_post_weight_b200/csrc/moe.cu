@@ -15,10 +15,12 @@ namespace nvfp4 {
 namespace {
 
 // ---- the sort ----------------------------------------------------------------
-constexpr int kSortWarps = 16;
-constexpr int kSortChunk = 4096;    // slots per CTA; at least NVFP4_MAX_EXPERTS
-constexpr int kSortMaxChunks = 512; // longer inputs take longer chunks
+constexpr int kSortWarps = 32;
+constexpr int kSortOneCta = 4096;   // slots that one CTA sorts by itself
+constexpr int kSortChunk = 1024;    // least slots per CTA beyond; at least NVFP4_MAX_EXPERTS
+constexpr int kSortMaxChunks = 128;
 static_assert(kSortChunk >= NVFP4_MAX_EXPERTS, "a chunk's counts lie in its own positions");
+static_assert(kSortWarps * 32 >= NVFP4_MAX_EXPERTS, "a thread per expert");
 
 // Expert of slot s, or n_experts for a slot without one.
 __device__ __forceinline__ int slot_expert(const void* ids, int wide, int64_t s, int n_experts) {
@@ -30,31 +32,35 @@ __device__ __forceinline__ int slot_expert(const void* ids, int wide, int64_t s,
   return v < 0 || v >= n_experts ? n_experts : v;
 }
 
-// Counts of one warp's slots [s0, s1) per expert into cnt (shared, zeroed);
-// kWrite: cnt holds the row where the warp's first slot of each expert goes,
-// and every slot's position and its row's token are written instead.
-template <bool kWrite>
-__device__ __forceinline__ void warp_slots(const void* ids, int wide, int64_t s0, int64_t s1,
-                                           int n_experts, int top_k, int* cnt, int32_t* rows,
-                                           int32_t* position) {
+// Adds one warp's slots [s0, s1) per expert to cnt (shared).
+__device__ __forceinline__ void count_slots(const void* ids, int wide, int64_t s0, int64_t s1,
+                                            int n_experts, int* cnt) {
+#pragma unroll 4
+  for (int64_t s = s0 + (threadIdx.x & 31); s < s1; s += 32) {
+    const int e = slot_expert(ids, wide, s, n_experts);
+    if (e < n_experts) atomicAdd(cnt + e, 1);
+  }
+}
+
+// Gives one warp's slots [s0, s1) their rows in order: next (shared) holds the
+// row where the warp's next slot of each expert goes.
+__device__ __forceinline__ void place_slots(const void* ids, int wide, int64_t s0, int64_t s1,
+                                            int n_experts, int top_k, int* next, int32_t* rows,
+                                            int32_t* position) {
   const int lane = threadIdx.x & 31;
   for (int64_t b = s0; b < s1; b += 32) {
     const int64_t s = b + lane;
     const int e = s < s1 ? slot_expert(ids, wide, s, n_experts) : n_experts;
     const unsigned same = __match_any_sync(0xffffffffu, e);
     const int before = __popc(same & ((1u << lane) - 1));
-    int base = 0;
-    if (e < n_experts) base = cnt[e];
+    int r = -1;
+    if (e < n_experts) r = next[e] + before;
     __syncwarp();
-    if (e < n_experts && before == 0) cnt[e] = base + __popc(same);
+    if (e < n_experts && before == 0) next[e] = r + __popc(same);
     __syncwarp();
-    if (kWrite && s < s1) {
-      if (e < n_experts) {
-        position[s] = base + before;
-        rows[base + before] = (int32_t)(s / top_k);
-      } else {
-        position[s] = -1;
-      }
+    if (s < s1) {
+      position[s] = r;
+      if (r >= 0) rows[r] = (int32_t)(s / top_k);
     }
   }
 }
@@ -83,12 +89,12 @@ __device__ __forceinline__ int cta_scan(int v, int* warp_sums) {
   if (lane == 31) warp_sums[w] = v;
   __syncthreads();
   if (w == 0) {
-    int t = lane < kSortWarps ? warp_sums[lane] : 0;
+    int t = warp_sums[lane];
     for (int d = 1; d < 32; d <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, t, d);
       if (lane >= d) t += u;
     }
-    if (lane < kSortWarps) warp_sums[lane] = t;
+    warp_sums[lane] = t;
   }
   __syncthreads();
   if (w > 0) v += warp_sums[w - 1];
@@ -110,21 +116,16 @@ __device__ __forceinline__ void counts_to_rows(int* cnt, int n_experts, const in
 }
 
 // Offsets of the experts from their totals (tot, shared; replaced by each
-// expert's first row); every thread of the CTA takes two neighbours.
+// expert's first row).
 __device__ __forceinline__ void scan_totals(int* tot, int n_experts, int* warp_sums,
                                             int32_t* offsets) {
-  const int e = 2 * threadIdx.x;
-  const int a = e < n_experts ? tot[e] : 0, b = e + 1 < n_experts ? tot[e + 1] : 0;
-  const int end = cta_scan(a + b, warp_sums);
+  const int e = threadIdx.x, n = e < n_experts ? tot[e] : 0;
+  const int end = cta_scan(n, warp_sums);
   if (e < n_experts) {
-    tot[e] = end - a - b;
-    offsets[e + 1] = end - b;
+    tot[e] = end - n;
+    offsets[e + 1] = end;
   }
-  if (e + 1 < n_experts) {
-    tot[e + 1] = end - b;
-    offsets[e + 2] = end;
-  }
-  if (threadIdx.x == 0) offsets[0] = 0;
+  if (e == 0) offsets[0] = 0;
   __syncthreads();
 }
 
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   int64_t w0, w1;
   warp_range(0, n, &w0, &w1);
   int* mine = cnt + (threadIdx.x >> 5) * n_experts;
-  warp_slots<false>(ids, wide, w0, w1, n_experts, top_k, mine, nullptr, nullptr);
+  count_slots(ids, wide, w0, w1, n_experts, mine);
   __syncthreads();
   for (int e = threadIdx.x; e < n_experts; e += blockDim.x) {
     int s = 0;
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   scan_totals(tot, n_experts, warp_sums, offsets);
   counts_to_rows(cnt, n_experts, tot);
   __syncthreads();
-  warp_slots<true>(ids, wide, w0, w1, n_experts, top_k, mine, rows, position);
+  place_slots(ids, wide, w0, w1, n_experts, top_k, mine, rows, position);
   // the rows behind the last expert's (the CTA's own write, read after a barrier)
   const int64_t kept = n_experts > 0 ? offsets[n_experts] : 0;
   for (int64_t r = kept + threadIdx.x; r < n; r += blockDim.x) rows[r] = -1;
@@ -162,45 +163,48 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 __global__ void __launch_bounds__(kSortWarps * 32)
     sort_count_kernel(const void* ids, int wide, int64_t n, int64_t chunk, int n_experts,
                       int32_t* position) {
-  extern __shared__ int cnt[];
-  for (int i = threadIdx.x; i < kSortWarps * n_experts; i += blockDim.x) cnt[i] = 0;
+  extern __shared__ int cnt[];   // n_experts
+  for (int i = threadIdx.x; i < n_experts; i += blockDim.x) cnt[i] = 0;
   __syncthreads();
   int64_t s0, s1, w0, w1;
   chunk_range(n, chunk, gridDim.x, blockIdx.x, &s0, &s1);
   warp_range(s0, s1, &w0, &w1);
-  warp_slots<false>(ids, wide, w0, w1, n_experts, 1, cnt + (threadIdx.x >> 5) * n_experts, nullptr,
-                    nullptr);
+  count_slots(ids, wide, w0, w1, n_experts, cnt);
   __syncthreads();
-  for (int e = threadIdx.x; e < n_experts; e += blockDim.x) {
-    int s = 0;
-    for (int w = 0; w < kSortWarps; ++w) s += cnt[w * n_experts + e];
-    position[s0 + e] = s;
-  }
+  for (int e = threadIdx.x; e < n_experts; e += blockDim.x) position[s0 + e] = cnt[e];
 }
 
 // One CTA: chunk counts -> each chunk's first row of each expert, and offsets.
+// parts threads share an expert's chunks.
 __global__ void __launch_bounds__(kSortWarps * 32)
-    sort_scan_kernel(int64_t chunk, int n_chunks, int n_experts, int32_t* offsets,
+    sort_scan_kernel(int64_t chunk, int n_chunks, int n_experts, int parts, int32_t* offsets,
                      int32_t* position) {
-  extern __shared__ int tot[];
+  extern __shared__ int sums[];   // parts x n_experts, then n_experts totals
   __shared__ int warp_sums[32];
+  int* tot = sums + parts * n_experts;
   pdl_wait();
-  for (int e = threadIdx.x; e < n_experts; e += blockDim.x) {
-    int s = 0;
+  const int e = threadIdx.x % n_experts, part = threadIdx.x / n_experts;
+  const int per = (n_chunks + parts - 1) / parts;
+  const int c0 = min(part * per, n_chunks), c1 = part < parts ? min(c0 + per, n_chunks) : c0;
+  int s = 0;
 #pragma unroll 8
-    for (int c = 0; c < n_chunks; ++c) s += position[c * chunk + e];
-    tot[e] = s;
+  for (int c = c0; c < c1; ++c) s += position[c * chunk + e];
+  if (part < parts) sums[threadIdx.x] = s;
+  __syncthreads();
+  if (part == 0) {
+    int t = 0;
+    for (int p = 0; p < parts; ++p) t += sums[p * n_experts + e];
+    tot[e] = t;
   }
   __syncthreads();
   scan_totals(tot, n_experts, warp_sums, offsets);
-  for (int e = threadIdx.x; e < n_experts; e += blockDim.x) {
-    int r = tot[e];
+  int r = tot[e];
+  for (int p = 0; p < part && p < parts; ++p) r += sums[p * n_experts + e];
 #pragma unroll 8
-    for (int c = 0; c < n_chunks; ++c) {
-      const int v = position[c * chunk + e];
-      position[c * chunk + e] = r;
-      r += v;
-    }
+  for (int c = c0; c < c1; ++c) {
+    const int v = position[c * chunk + e];
+    position[c * chunk + e] = r;
+    r += v;
   }
 }
 
@@ -215,13 +219,13 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   chunk_range(n, chunk, gridDim.x, blockIdx.x, &s0, &s1);
   warp_range(s0, s1, &w0, &w1);
   int* mine = cnt + (threadIdx.x >> 5) * n_experts;
-  warp_slots<false>(ids, wide, w0, w1, n_experts, top_k, mine, nullptr, nullptr);
+  count_slots(ids, wide, w0, w1, n_experts, mine);
   pdl_wait();
   for (int e = threadIdx.x; e < n_experts; e += blockDim.x) first[e] = position[s0 + e];
   __syncthreads();   // every thread has its counts: the positions may be written
   counts_to_rows(cnt, n_experts, first);
   __syncthreads();
-  warp_slots<true>(ids, wide, w0, w1, n_experts, top_k, mine, rows, position);
+  place_slots(ids, wide, w0, w1, n_experts, top_k, mine, rows, position);
   const int64_t kept = offsets[n_experts];
   for (int64_t r = kept + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < n;
        r += (int64_t)gridDim.x * blockDim.x)
@@ -229,59 +233,98 @@ __global__ void __launch_bounds__(kSortWarps * 32)
 }
 
 // ---- rows there and back -------------------------------------------------------
-// V elements of T at p (V * sizeof(T) bytes, aligned to that), as floats.
+// V elements of a row: consecutive ones in one access where every row starts on
+// its boundary (kVec), else V elements one thread of 256 (32) apart, so that a
+// warp's accesses stay whole and V of them are in flight either way.
 template <typename T, int V>
-struct Vec {
-  alignas(sizeof(T) * V) T v[V];
+struct alignas(sizeof(T) * V) Vec {
+  T v[V];
 };
+template <typename T, int V, bool kVec, int kApart>
+__device__ __forceinline__ void load_row(const T* row, int64_t c, int64_t d, T* v) {
+  if (kVec) {
+    *reinterpret_cast<Vec<T, V>*>(v) = *reinterpret_cast<const Vec<T, V>*>(row + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + i * kApart < d) v[i] = row[c + i * kApart];
+  }
+}
+template <typename T, int V, bool kVec, int kApart>
+__device__ __forceinline__ void store_row(T* row, int64_t c, int64_t d, const T* v) {
+  if (kVec) {
+    *reinterpret_cast<Vec<T, V>*>(row + c) = *reinterpret_cast<const Vec<T, V>*>(v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c + i * kApart < d) row[c + i * kApart] = v[i];
+  }
+}
+// First of the V columns of thread t of `threads` in block b of V * threads.
+template <int V, bool kVec>
+__device__ __forceinline__ int64_t first_column(int64_t b, int t, int threads) {
+  return b * V * threads + (kVec ? t * V : t);
+}
 
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
 // Token blockIdx.x's row to the sorted rows of its slots: one read, top_k writes.
-template <typename T>   // T: the bytes one thread moves
+template <typename T, int V, bool kVec>
 __global__ void __launch_bounds__(256)
     gather_kernel(const T* __restrict__ X, const int32_t* __restrict__ position, int top_k,
-                  int64_t n_slots, int64_t cols, T* __restrict__ Xs) {
+                  int64_t n_slots, int64_t d, T* __restrict__ Xs) {
   const int64_t t = blockIdx.x;
-  for (int64_t c = (int64_t)blockIdx.y * blockDim.x + threadIdx.x; c < cols;
-       c += (int64_t)gridDim.y * blockDim.x) {
-    const T v = X[t * cols + c];
+  for (int64_t b = blockIdx.y; b * V * 256 < d; b += gridDim.y) {
+    const int64_t c = first_column<V, kVec>(b, threadIdx.x, 256);
+    if (c >= d) break;
+    alignas(16) T v[V];
+    load_row<T, V, kVec, 256>(X + t * d, c, d, v);
     for (int j = 0; j < top_k; ++j) {
       const int64_t p = position[t * top_k + j];
-      if (p >= 0 && p < n_slots) Xs[p * cols + c] = v;
+      if (p >= 0 && p < n_slots) store_row<T, V, kVec, 256>(Xs + p * d, c, d, v);
     }
   }
 }
 
 // Y[t] = sum_j w[t, j] Ys[position[t, j]] in fp32, j ascending; one rounding.
-template <typename TS, typename TY, int V>
+template <typename TS, typename TY, int V, bool kVec>
 __global__ void __launch_bounds__(256)
     combine_kernel(const TS* __restrict__ Ys, const int32_t* __restrict__ position,
                    const float* __restrict__ weights, int top_k, int64_t n_slots, int64_t d,
                    TY* __restrict__ Y) {
+  constexpr int kAhead = sizeof(TS) == 4 ? 8 : 4;   // 32 registers of rows
   const int64_t t = blockIdx.x;
-  for (int64_t c = ((int64_t)blockIdx.y * blockDim.x + threadIdx.x) * V; c < d;
-       c += (int64_t)gridDim.y * blockDim.x * V) {
+  for (int64_t b = blockIdx.y; b * V * 256 < d; b += gridDim.y) {
+    const int64_t c = first_column<V, kVec>(b, threadIdx.x, 256);
+    if (c >= d) break;
     float acc[V] = {};
-#pragma unroll 4
-    for (int j = 0; j < top_k; ++j) {
-      const int64_t p = position[t * top_k + j];
-      if (p < 0 || p >= n_slots) continue;
-      const float w = weights ? weights[t * top_k + j] : 1.f;
-      const Vec<TS, V> y = *reinterpret_cast<const Vec<TS, V>*>(Ys + p * d + c);
+    for (int j0 = 0; j0 < top_k; j0 += kAhead) {
+      int64_t p[kAhead];
+      alignas(16) TS y[kAhead][V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = fmaf(w, as_f32(y.v[i]), acc[i]);
+      for (int j = 0; j < kAhead; ++j) {
+        p[j] = j0 + j < top_k ? position[t * top_k + j0 + j] : -1;
+        if (p[j] >= n_slots) p[j] = -1;
+        if (p[j] >= 0) load_row<TS, V, kVec, 256>(Ys + p[j] * d, c, d, y[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (p[j] < 0) continue;
+        const float w = weights ? weights[t * top_k + j0 + j] : 1.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(w, as_f32(y[j][i]), acc[i]);
+      }
     }
-    Vec<TY, V> o;
+    alignas(16) TY o[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) o.v[i] = (TY)acc[i];
-    *reinterpret_cast<Vec<TY, V>*>(Y + t * d + c) = o;
+    for (int i = 0; i < V; ++i) o[i] = (TY)acc[i];
+    store_row<TY, V, kVec, 256>(Y + t * d, c, d, o);
   }
 }
 
 // One warp per slot: dYs[p] = w dY[t], dw = <dY[t], Ys[p]> (fp32).
-template <typename T, int V>
+template <typename T, int V, bool kVec>
 __global__ void __launch_bounds__(256)
     combine_backward_kernel(const T* __restrict__ dY, const T* __restrict__ Ys,
                             const int32_t* __restrict__ position,
@@ -295,18 +338,20 @@ __global__ void __launch_bounds__(256)
   if (p >= 0 && p < n_slots) {
     const float w = weights[s];
     const int64_t t = s / top_k;
+    // (columns of one step lie in each row V at a time, or 32 apart)
 #pragma unroll 4
-    for (int64_t c = (int64_t)lane * V; c < d; c += 32 * V) {
-      const Vec<T, V> g = *reinterpret_cast<const Vec<T, V>*>(dY + t * d + c);
-      const Vec<T, V> y = *reinterpret_cast<const Vec<T, V>*>(Ys + p * d + c);
-      Vec<T, V> o;
+    for (int64_t c = kVec ? lane * V : lane; c < d; c += 32 * V) {
+      alignas(16) T g[V], y[V], o[V];
+      load_row<T, V, kVec, 32>(dY + t * d, c, d, g);
+      load_row<T, V, kVec, 32>(Ys + p * d, c, d, y);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float gi = as_f32(g.v[i]);
-        dot = fmaf(gi, as_f32(y.v[i]), dot);
-        o.v[i] = (T)(w * gi);
+        const bool in = kVec || c + i * 32 < d;
+        const float gi = in ? as_f32(g[i]) : 0.f;
+        if (in) dot = fmaf(gi, as_f32(y[i]), dot);
+        o[i] = (T)(w * gi);
       }
-      *reinterpret_cast<Vec<T, V>*>(dYs + p * d + c) = o;
+      store_row<T, V, kVec, 32>(dYs + p * d, c, d, o);
     }
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
   }
@@ -328,17 +373,37 @@ nvfp4_status check_slots(int64_t n_tok, int64_t top_k) {
 
 // CTAs along the columns: one per 256 threads' worth, at most 8 (a token's CTAs
 // all read its positions).
-unsigned col_blocks(int64_t items) {
-  const int64_t b = (items + 255) / 256;
-  return (unsigned)(b < 1 ? 1 : b > 8 ? 8 : b);
+unsigned col_blocks(int64_t d, int V) {
+  const int64_t b = (d + 256 * V - 1) / (256 * V);
+  return (unsigned)(b > 8 ? 8 : b);
 }
 
 template <typename TS, typename TY, int V>
-void launch_combine(const void* Ys, const int32_t* pos, const float* w, int64_t n_tok, int top_k,
-                    int64_t d, void* Y, cudaStream_t st) {
-  const dim3 grid((unsigned)n_tok, col_blocks((d + V - 1) / V));
-  combine_kernel<TS, TY, V><<<grid, 256, 0, st>>>(static_cast<const TS*>(Ys), pos, w, top_k,
-                                                  n_tok * top_k, d, static_cast<TY*>(Y));
+void launch_combine(bool vec, const void* Ys, const int32_t* pos, const float* w, int64_t n_tok,
+                    int top_k, int64_t d, void* Y, cudaStream_t st) {
+  const dim3 grid((unsigned)n_tok, col_blocks(d, V));
+  auto kernel = vec ? combine_kernel<TS, TY, V, true> : combine_kernel<TS, TY, V, false>;
+  kernel<<<grid, 256, 0, st>>>(static_cast<const TS*>(Ys), pos, w, top_k, n_tok * top_k, d,
+                               static_cast<TY*>(Y));
+}
+
+template <typename T, int V>
+void launch_gather(bool vec, const void* X, const int32_t* pos, int64_t n_tok, int top_k, int64_t d,
+                   void* Xs, cudaStream_t st) {
+  const dim3 grid((unsigned)n_tok, col_blocks(d, V));
+  auto kernel = vec ? gather_kernel<T, V, true> : gather_kernel<T, V, false>;
+  kernel<<<grid, 256, 0, st>>>(static_cast<const T*>(X), pos, top_k, n_tok * top_k, d,
+                               static_cast<T*>(Xs));
+}
+
+template <typename T, int V>
+void launch_backward(bool vec, const void* dY, const void* Ys, const int32_t* pos, const float* w,
+                     int64_t n_tok, int top_k, int64_t d, void* dYs, float* dw, cudaStream_t st) {
+  const int64_t n = n_tok * top_k;
+  auto kernel = vec ? combine_backward_kernel<T, V, true> : combine_backward_kernel<T, V, false>;
+  kernel<<<(unsigned)((n + 7) / 8), 256, 0, st>>>(static_cast<const T*>(dY),
+                                                  static_cast<const T*>(Ys), pos, w, top_k, n, d,
+                                                  static_cast<T*>(dYs), dw);
 }
 
 }  // namespace
@@ -369,12 +434,10 @@ nvfp4_status nvfp4_moe_sort(const void* expert_ids, int id_bytes, int64_t n_tok,
     // (per device and kernel; setting it again is harmless)
     NVFP4_CUDA_TRY(cudaFuncSetAttribute(sort_small_kernel,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-    NVFP4_CUDA_TRY(cudaFuncSetAttribute(sort_count_kernel,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     NVFP4_CUDA_TRY(cudaFuncSetAttribute(sort_place_kernel,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
   }
-  if (n < 2 * kSortChunk || E == 0) {
+  if (n <= kSortOneCta || E == 0) {
     sort_small_kernel<<<1, block, smem, st>>>(expert_ids, wide, n, E, k, offsets, rows, position);
     NVFP4_LAUNCH_CHECK();
     count_launches(1);
@@ -383,10 +446,11 @@ nvfp4_status nvfp4_moe_sort(const void* expert_ids, int id_bytes, int64_t n_tok,
   int64_t chunk = (n + kSortMaxChunks - 1) / kSortMaxChunks;
   if (chunk < kSortChunk) chunk = kSortChunk;
   const int n_chunks = (int)(n / chunk);
-  sort_count_kernel<<<n_chunks, block, smem, st>>>(expert_ids, wide, n, chunk, E, position);
+  sort_count_kernel<<<n_chunks, block, sizeof(int) * E, st>>>(expert_ids, wide, n, chunk, E, position);
   NVFP4_LAUNCH_CHECK();
-  NVFP4_CUDA_TRY(launch_chained(sort_scan_kernel, dim3(1), block, sizeof(int) * E, st, chunk,
-                                n_chunks, E, offsets, position));
+  const int parts = kSortWarps * 32 / E;
+  NVFP4_CUDA_TRY(launch_chained(sort_scan_kernel, dim3(1), block, sizeof(int) * (parts + 1) * E, st,
+                                chunk, n_chunks, E, parts, offsets, position));
   NVFP4_CUDA_TRY(launch_chained(sort_place_kernel, dim3(n_chunks), block, smem, st, expert_ids, wide,
                                 n, chunk, E, k, (const int32_t*)offsets, rows, position));
   count_launches(3);
@@ -406,20 +470,11 @@ nvfp4_status nvfp4_moe_gather(const void* X, nvfp4_dtype dtype, const int32_t* p
     return NVFP4_ERR_INVALID_ARG;
   cudaStream_t st = as_cuda(stream);
   ProfileScope ps(kPhaseRoute, st);
-  const uintptr_t all = reinterpret_cast<uintptr_t>(X) | reinterpret_cast<uintptr_t>(Xs) | row;
-  const int64_t n = n_tok * top_k;
-  // the widest access that the rows' length and the bases allow
-  if (all % 16 == 0)
-    gather_kernel<uint4><<<dim3((unsigned)n_tok, col_blocks(row / 16)), 256, 0, st>>>(
-        static_cast<const uint4*>(X), position, (int)top_k, n, row / 16, static_cast<uint4*>(Xs));
-  else if (all % 4 == 0)
-    gather_kernel<uint32_t><<<dim3((unsigned)n_tok, col_blocks(row / 4)), 256, 0, st>>>(
-        static_cast<const uint32_t*>(X), position, (int)top_k, n, row / 4,
-        static_cast<uint32_t*>(Xs));
+  const bool vec = row % 16 == 0 && is_aligned(X, 16) && is_aligned(Xs, 16);
+  if (dtype == NVFP4_BF16)
+    launch_gather<__nv_bfloat16, 8>(vec, X, position, n_tok, (int)top_k, d, Xs, st);
   else
-    gather_kernel<uint16_t><<<dim3((unsigned)n_tok, col_blocks(row / 2)), 256, 0, st>>>(
-        static_cast<const uint16_t*>(X), position, (int)top_k, n, row / 2,
-        static_cast<uint16_t*>(Xs));
+    launch_gather<float, 4>(vec, X, position, n_tok, (int)top_k, d, Xs, st);
   NVFP4_LAUNCH_CHECK();
   count_launches(1);
   return NVFP4_OK;
@@ -438,21 +493,16 @@ nvfp4_status nvfp4_moe_combine(const void* Ys, nvfp4_dtype s_dtype, const int32_
     return NVFP4_ERR_INVALID_ARG;
   cudaStream_t st = as_cuda(stream);
   ProfileScope ps(kPhaseRoute, st);
-  // 8 (bf16) or 4 columns a thread where every row of both sides starts aligned for it
   const bool vec = d % 8 == 0 && is_aligned(Ys, 16) && is_aligned(Y, 16);
   const int k = (int)top_k;
-#define NVFP4_COMBINE(TS, TY, V)                                                            \
-  (vec ? launch_combine<TS, TY, V>(Ys, position, weights, n_tok, k, d, Y, st)               \
-       : launch_combine<TS, TY, 1>(Ys, position, weights, n_tok, k, d, Y, st))
   if (s_dtype == NVFP4_BF16 && y_dtype == NVFP4_BF16)
-    NVFP4_COMBINE(__nv_bfloat16, __nv_bfloat16, 8);
+    launch_combine<__nv_bfloat16, __nv_bfloat16, 8>(vec, Ys, position, weights, n_tok, k, d, Y, st);
   else if (s_dtype == NVFP4_BF16)
-    NVFP4_COMBINE(__nv_bfloat16, float, 4);
+    launch_combine<__nv_bfloat16, float, 4>(vec, Ys, position, weights, n_tok, k, d, Y, st);
   else if (y_dtype == NVFP4_BF16)
-    NVFP4_COMBINE(float, __nv_bfloat16, 4);
+    launch_combine<float, __nv_bfloat16, 4>(vec, Ys, position, weights, n_tok, k, d, Y, st);
   else
-    NVFP4_COMBINE(float, float, 4);
-#undef NVFP4_COMBINE
+    launch_combine<float, float, 4>(vec, Ys, position, weights, n_tok, k, d, Y, st);
   NVFP4_LAUNCH_CHECK();
   count_launches(1);
   return NVFP4_OK;
@@ -473,26 +523,13 @@ nvfp4_status nvfp4_moe_combine_backward(const void* dY, const void* Ys, nvfp4_dt
     return NVFP4_ERR_INVALID_ARG;
   cudaStream_t st = as_cuda(stream);
   ProfileScope ps(kPhaseRoute, st);
-  const int64_t n = n_tok * top_k;
-  const unsigned grid = (unsigned)((n + 7) / 8);
   const bool vec = (size * d) % 16 == 0 && is_aligned(dY, 16) && is_aligned(Ys, 16) &&
                    is_aligned(dYs, 16);
-#define NVFP4_BACKWARD(T, V)                                                                     \
-  combine_backward_kernel<T, V><<<grid, 256, 0, st>>>(                                           \
-      static_cast<const T*>(dY), static_cast<const T*>(Ys), position, weights, (int)top_k, n, d, \
-      static_cast<T*>(dYs), dweights)
-  if (dtype == NVFP4_BF16) {
-    if (vec)
-      NVFP4_BACKWARD(__nv_bfloat16, 8);
-    else
-      NVFP4_BACKWARD(__nv_bfloat16, 1);
-  } else {
-    if (vec)
-      NVFP4_BACKWARD(float, 4);
-    else
-      NVFP4_BACKWARD(float, 1);
-  }
-#undef NVFP4_BACKWARD
+  const int k = (int)top_k;
+  if (dtype == NVFP4_BF16)
+    launch_backward<__nv_bfloat16, 8>(vec, dY, Ys, position, weights, n_tok, k, d, dYs, dweights, st);
+  else
+    launch_backward<float, 4>(vec, dY, Ys, position, weights, n_tok, k, d, dYs, dweights, st);
   NVFP4_LAUNCH_CHECK();
   count_launches(1);
   return NVFP4_OK;

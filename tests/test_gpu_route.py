@@ -47,7 +47,8 @@ def sort(ids, E, fill=99):
 
 
 SORTS = [(1, 1, 1), (1, 8, 128), (7, 3, 5), (64, 8, 128), (33, 2, 1024), (513, 1, 2), (1000, 8, 160),
-         (1023, 8, 128), (1024, 8, 128), (1025, 8, 1024), (4099, 6, 31), (65536, 8, 128)]
+         (1023, 8, 128), (1024, 8, 128), (1025, 8, 1024), (4099, 6, 31), (8192, 8, 128),
+         (8193, 8, 1024), (65537, 1, 700), (65536, 8, 128)]
 
 
 @pytest.mark.parametrize("T,k,E", SORTS)
@@ -70,7 +71,7 @@ def test_sort_extremes():
 
 
 def test_sort_long_chunks():
-    """Beyond 512 chunks of 4096 slots: longer chunks."""
+    """So many slots that a CTA takes more than the least number of them."""
     rng = np.random.default_rng(0)
     ids = rng.integers(-1, 40, (2 ** 18 + 3, 9)).astype(np.int32)
     E = 40
