@@ -474,20 +474,22 @@ nvfp4_status nvfp4_dequant_batched(int count, const uint8_t* const* codes,
  * Y       : n_tok x d_out, bf16 or fp32 (y_dtype, its own choice), fully
  *           written; must not overlap X.  d_in == 0 gives zeros.
  * ws      : workspace of nvfp4_gemv_workspace_size(n_tok, d_out, d_in, 0,
- *           0, x_dtype) bytes, 256-byte aligned (0 for calls that need none, NULL is
- *           then fine).  Its first
- *           int is the status word (nvfp4_workspace_status): a timed-out wait
- *           sets NVFP4_ERR_TIMEOUT, Y is then unspecified.
+ *           0, x_dtype) bytes, 256-byte aligned (0 for calls that need none,
+ *           NULL is then fine).  Its first int is the status word
+ *           (nvfp4_workspace_status): a timed-out wait sets
+ *           NVFP4_ERR_TIMEOUT, Y is then unspecified.
  * The products are exact, their sums fp32, and Y is rounded once.  Calls that
  * need a workspace run on the block-scaled FP4 tensor cores where codes and
  * scales are 16-byte aligned: there a (bf16) token's entry is kept to 2^-22 of
  * the largest of its block of 16 columns, or to 2^-39 of the token's largest
  * where that is more (entries within 2^-14 of their block's largest are
  * exact); elsewhere tokens are used at all their bits.  NaN and infinite
- * tokens behave as in the plain product and stay in their row, and scale code
- * 127 (a NaN, which the quantize call does not write) may give any value in
- * its column.  Made for few tokens, where the weights' bytes bound the
- * product; any n_tok is right.
+ * tokens behave as in the plain product and stay in their row; tokens beyond
+ * 2^120 may overflow on the way, and scale code 127 (a NaN, which the quantize
+ * call does not write) may give any value in its column.  Made for few tokens,
+ * where the weights' bytes bound the product; any n_tok is right, but from some
+ * hundred on a dequantised copy and a GEMM are faster.  Calls that may overlap
+ * (two streams) need a workspace each.
  * d_out, n_tok <= 2^22, d_in <= 2^17 (NVFP4_ERR_SHAPE beyond). */
 nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const uint8_t* codes,
                         const uint8_t* scales, const float* global_scale, int64_t d_out,
@@ -615,8 +617,9 @@ long long nvfp4_launch_count(void);
 
 /* Debugging support (the paper has no counterpart; it stands in for a memory
  * checker).  The library is also built as libnvfp4pw_debug.so with
- * NVFP4_DEBUG defined: there every kernel checks the tile and index
- * arithmetic it derives from the call's shapes (a tile decomposition that
+ * NVFP4_DEBUG defined: there the kernels of the solve, and of the products
+ * that take a workspace, check the tile and index arithmetic they derive
+ * from the call's shapes (a tile decomposition that
  * leaves its output, a row or column past the array) before each access; a
  * failed check skips the access and records NVFP4_ERR_BOUNDS in the call's
  * status word (for the tensor-core Hessian: the status nvfp4_hessian_status

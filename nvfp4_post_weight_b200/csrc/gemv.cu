@@ -18,6 +18,17 @@
 // each share the tokens' slice; the slices of K are the CTAs of a cluster,
 // which add up their sums through distributed shared memory in a fixed order:
 // no workspace, no atomics, the same bits every time.
+//
+// This kernel takes what the FP4 path (gemv_fp4.cu) does not: fp32 tokens, rows
+// that are not whole panels of 256 columns, other alignments, and sizes that are
+// over before that path's chain of stages is.  What bounds it there is latency
+// (1024 x 8192, one token: 4.7 MB in 6.5 us, of which a launch, a DRAM access, the
+// staging of the tokens and the join take five); with more weights the issue of
+// some 3.7 instructions per weight (the 28672 x 8192 pair: 86 us).  fp16 operands
+// by the e2m1 conversion instruction needed 2.5 per weight and took longer (94
+// us: the conversion is issued at a fraction of the rate), as did a persistent
+// form with the codes copied to shared memory (77 us for the pair, but 708 us
+// where this takes 305: 64 tokens' rows through 128 experts' pairs).
 #include <cooperative_groups.h>
 
 #include "gemv.cuh"

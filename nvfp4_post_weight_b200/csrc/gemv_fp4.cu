@@ -14,11 +14,21 @@
 // it), and bf16 entries within 2^-14 of their block's largest are exact.  (fp32
 // tokens would lose bits of every entry; they take the other kernel.)
 //
-// The weights' bytes bound the product: nothing is decoded, a warp's lanes issue
-// the copies and one thread the matrix instructions.  One CTA per SM streams
-// rows of its own, equal to eight rows over all SMs, in tiles of 128 (an M =
-// 128 instruction may have rows that are not there: rows do not mix), 256
-// columns of K a stage.
+// Nothing is decoded: one warp has the weights copied, one the digits, one issues
+// the matrix instructions (an N <= 64 takes 45 cycles, N = 128 64), three groups
+// of four warps bring the block scales to tensor memory (and read the sums).  One
+// CTA per SM streams rows of its own, equal to eight rows over all SMs, as tiles
+// of up to 128 rows (an M = 128 instruction may have rows that are not there: rows
+// do not mix), 256 or 512 columns of K a stage.  A split of K over a cluster
+// would need its sums joined; it is not needed to fill the SMs.
+//
+// What bounds it: one token's DRAM bytes (the 28672 x 8192 pair, 264 MB in 49.6
+// us, 82% of the copy rate); with more tokens the traffic from L2 to the SMs, where
+// every CTA reads all digits, four bytes an entry, beside its rows (the pair with
+// 32 tokens, two passes, 0.84 GB in 94 us); with few rows an SM the chain of
+// stages (some 0.25 us per 256 columns).  Loading scales through registers instead
+// of TMA took 58 us for the one-token pair, copies of scales by tcgen05.cp from
+// the issuing thread 95 us, a single warp lane's non-uniform loop 68 us.
 #include <cuda_bf16.h>
 #include <string.h>
 
@@ -33,9 +43,21 @@ using namespace sm100;
 constexpr int kPanelK = 256;                      // columns of K in a 128-byte row of codes
 constexpr int kMaxPanels = 2;                     // panels per stage
 constexpr int kMaxStages = 12;
-constexpr int kGroups = 3;                        // groups of four warps that move scales and
-constexpr int kWorkers = 4 * kGroups;             // read sums
-constexpr int kThreads = (kWorkers + 3) * 32;
+constexpr int kGroups = 3;                        // groups of four warps that move scales
+// Warps by role: the groups, with one matrix four more that read its sums, one each
+// for the codes' copies, the matrix instructions and the digits' copies.  With two
+// matrices the groups read the sums too, a third of the tokens each: their
+// accumulator mostly has no second one beside it, so that reading it has to be
+// quick (64 tokens' rows through 128 experts' pairs: 146 us, 165 us with warps of
+// their own); with one matrix and few columns of K the scales of the next tile then
+// waited for them (the down projections: 100 us, 84 us now).
+template <int NW>
+struct Roles {
+  static constexpr bool kOwnSums = NW == 1;
+  static constexpr int kSumWarp = 4 * kGroups, kCodeWarp = kSumWarp + (kOwnSums ? 4 : 0),
+                       kMmaWarp = kCodeWarp + 1, kDigitWarp = kMmaWarp + 1,
+                       kThreads = (kDigitWarp + 1) * 32;
+};
 constexpr int64_t kMaxRows = 2048;                // sorted rows that are taken apart at a time
 constexpr int kTile = 128;
 constexpr int kUnit = 8;                          // output columns that are shared out together
@@ -243,16 +265,18 @@ __device__ __forceinline__ void mma_nvfp4(uint32_t d, uint64_t a, uint64_t b, ui
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
+__device__ __forceinline__ void tmem_ld8_twice(uint32_t ta, uint32_t tb, float (*v)[8]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%8,%9,%10,%11,%12,%13,%14,%15}, [%17];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(ta), "r"(tb)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 16; ++i) v[i >> 3][i & 7] = __uint_as_float(r[i]);
 }
 
 // What one CTA works through: pieces of (expert, pass over its tokens), each a
@@ -277,16 +301,23 @@ struct Pieces {
       u_end = all * (b + 1) / ctas;
     }
   }
-  // Warp-wide.
+  // Warp-wide.  (The debug build leaves out a piece that is not inside the call's
+  // arrays, in every role alike.)
   __device__ __forceinline__ bool next(const Fp4Args& a, Piece* q) {
-    if (u >= u_end) return false;
-    const int64_t slot = u / units, ub = u - slot * units;
-    const int64_t ue = min(units, u_end - slot * units);
-    u = slot * units + ue;
-    find_pass(a.p, a.tokens, (int)slot, &q->e, &q->t0, &q->n);
-    q->row0 = ub * kUnit;
-    q->row1 = min(ue * kUnit, a.p.d_out);
-    return true;
+    while (u < u_end) {
+      const int64_t slot = u / units, ub = u - slot * units;
+      const int64_t ue = min(units, u_end - slot * units);
+      u = slot * units + ue;
+      const bool found = find_pass(a.p, a.tokens, (int)slot, &q->e, &q->t0, &q->n);
+      q->row0 = ub * kUnit;
+      q->row1 = min(ue * kUnit, a.p.d_out);
+      if (NVFP4_DCHECK(found && q->e >= 0 && q->e < a.p.n_experts && q->n > 0 &&
+                           q->n <= a.tokens && q->t0 >= 0 && q->t0 + q->n <= a.p.n_rows &&
+                           q->row0 < q->row1,
+                       a.status))
+        return true;
+    }
+    return false;
   }
 };
 
@@ -309,12 +340,16 @@ __device__ __noinline__ float plain_product(const Product& p, int w, int e, int6
 }
 
 template <int NW>
-__global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_constant__ Fp4Args a) {
+__global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
+    product_fp4_kernel(const __grid_constant__ Fp4Args a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~uintptr_t(1023));
   __shared__ Shared shared;
   Shared* sh = &shared;
+  constexpr int kSumWarp = Roles<NW>::kSumWarp, kCodeWarp = Roles<NW>::kCodeWarp,
+                kMmaWarp = Roles<NW>::kMmaWarp, kDigitWarp = Roles<NW>::kDigitWarp;
+  constexpr bool kOwnSums = Roles<NW>::kOwnSums;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int P = a.panels, S = a.ring, K = a.n_stages;
   const int columns = (a.tokens + 1) / 2 * 16;   // of an accumulator, per matrix
@@ -337,13 +372,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->d_full[i], 1);
-      mbar_init(&sh->d_empty[i], kWorkers);
+      mbar_init(&sh->d_empty[i], kOwnSums ? 4 : 4 * kGroups);
     }
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     fence_mbar_init();
   }
-  if (warp == kWorkers + 1) tmem_alloc(&sh->tmem, kTmemCols);
+  if (warp == kMmaWarp) tmem_alloc(&sh->tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -367,7 +402,55 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
     }
   };
 
-  if (warp == kWorkers) {
+  // The sums of tile no. g at output columns row ..: thread = column (TMEM lane),
+  // tokens first, first + apart, ...  Warp-wide.  Each lane keeps the exponent of one
+  // of the pass' tokens (32 at most): fetched when its token's turn comes, they took
+  // the down projections of 64 tokens 18 us longer.  Two sums a round trip to tensor
+  // memory instead of one: 88 to 84 us.
+  int exponent = 0;
+  float sg[NW];
+  auto enter_pass = [&](const Piece& q) {
+    exponent = lane < q.n ? __ldg(a.expo + q.t0 + lane) : 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) sg[w] = __ldg(a.p.sg[w] + q.e);
+  };
+  auto read_sums = [&](const Piece& q, int64_t row, int g, int first, int apart) {
+    const int buf = a.d_bufs == 2 ? g & 1 : 0, use = a.d_bufs == 2 ? g >> 1 : g;
+    if (!wait(&sh->d_full[buf], use & 1, limit, sh)) return false;
+    tc_fence_after();
+    const int64_t o = row + (threadIdx.x & (kTile - 1)), o_end = min(row + a.tile, q.row1);
+    const uint32_t d = tmem + ((uint32_t)((warp & 3) * 32) << 16) + buf * NW * columns;
+    // two sums at a time: both matrices' of a token, or one matrix' of two tokens
+    constexpr int kTokens = 2 / NW;
+    for (int i0 = first; i0 < q.n; i0 += apart * kTokens) {
+      float c[2][8], v[2];
+      const int second = min(i0 + apart, q.n - 1);
+      tmem_ld8_twice(d + 8 * i0, NW == 2 ? d + columns + 8 * i0 : d + 8 * second, c);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int w = k * (NW - 1), i = NW == 2 || k == 0 ? i0 : second;
+        const int E = __shfl_sync(~0u, exponent, i);
+        float sum = c[k][7];
+#pragma unroll
+        for (int p = 6; p >= 0; --p) sum = fmaf(sum, 8.f, c[k][p]);
+        if (o < o_end) {
+          const double scale = __hiloint2double((E - 29 + 1023) << 20, 0);
+          v[k] = E == kNonFinite ? plain_product(a.p, w, q.e, x_row(a.p, q.t0 + i), o)
+                                 : (float)((double)sum * (scale * (double)sg[w]));
+        }
+      }
+      if (o < o_end) {
+        write_product<NW>(a.p, v, q.t0 + i0, o);
+        if (NW == 1 && i0 + apart < q.n) write_product<NW>(a.p, v + 1, q.t0 + second, o);
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->d_empty[buf]);
+    return true;
+  };
+
+  if (warp == kCodeWarp) {
     // ---------------------------------------------------------------- codes and their scales
     int issued = 0;
     bool ok = true;
@@ -407,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
       }
     }
     if (!ok) drain_copies(sh->weights, issued);
-  } else if (warp == kWorkers + 2) {
+  } else if (warp == kDigitWarp) {
     // ---------------------------------------------------------------- digits
     pdl_wait();
     int issued = 0;
@@ -438,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
       }
     }
     if (!ok) drain_copies(sh->tokens, issued);
-  } else if (warp == kWorkers + 1) {
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- matrix instructions
     int g = 0, sf = 0;   // accumulators so far, buffer of scales
     bool ok = true;
@@ -496,17 +579,17 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
     if (elect()) mma_commit(&sh->drain);
     __syncwarp();
     mbar_wait_drain(&sh->drain, 0);
-  } else {
-    // ---------------------------------------------------------------- scales, sums
+  } else if (warp < kSumWarp) {
+    // ---------------------------------------------------------------- scales
     // Groups of four warps, one warp per quarter of TMEM's lanes: lane l of each
     // quarter gets, per 64 columns of K, the words of rows l, l + 32, l + 64 and
     // l + 96.  A group takes the stages of its slots (a stage takes a group some
     // 700 cycles, the matrix instructions 400; a slot's stages all fall to one
-    // group, which so sees each phase of its barriers), and every third token of a
-    // tile's sums.
-    const int r = threadIdx.x & (kTile - 1), group = threadIdx.x >> 7;
+    // group, which so sees each phase of its barriers).
+    const int group = warp >> 2;
     const uint32_t quarter = (uint32_t)((warp & 3) * 32) << 16;
-    pdl_wait();   // (for the tokens' exponents)
+    if (!kOwnSums) pdl_wait();   // (for the tokens' exponents)
+    int g = 0;                          // accumulators so far
     int stage_no = 0, sf = 0, os = 0;   // stages so far, buffer of scales, slot of its last stage
     uint32_t oph = 0;
     auto get = [&](const uint8_t* p, int bytes_apart, uint4* v) {
@@ -521,9 +604,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
       v[2] = make_uint4(x[0].z, x[1].z, x[2].z, x[3].z);
       v[3] = make_uint4(x[0].w, x[1].w, x[2].w, x[3].w);
     };
-    int g = 0;
     bool ok = true;
     while (ok && pieces.next(a, &q)) {
+      if (!kOwnSums) enter_pass(q);
       for (int64_t row = q.row0; ok && row < q.row1; row += a.tile, ++g) {
         for (int st = 0; st < K; ++st) {
           const int slot = s, buf = sf, no = stage_no, free_slot = os;
@@ -560,43 +643,24 @@ __global__ void __launch_bounds__(kThreads, 1) product_fp4_kernel(const __grid_c
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->scaled[slot]);
         }
-        // the sums of the tile: thread = output column, the group's tokens
-        const int buf = a.d_bufs == 2 ? g & 1 : 0, use = a.d_bufs == 2 ? g >> 1 : g;
-        ok = ok && wait(&sh->d_full[buf], use & 1, limit, sh);
-        if (!ok) {
-          give_up(sh, a.status);
-          break;
-        }
-        tc_fence_after();
-        const int64_t o = row + r, o_end = min(row + a.tile, q.row1);
-        const uint32_t d = tmem + quarter + buf * NW * columns;
-        for (int i = group; i < q.n; i += kGroups) {
-          const int E = __ldg(a.expo + q.t0 + i);
-          float v[NW];
-#pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            float c[8];
-            tmem_ld8(d + w * columns + 8 * i, c);
-            float sum = c[7];
-#pragma unroll
-            for (int p = 6; p >= 0; --p) sum = fmaf(sum, 8.f, c[p]);
-            if (o < o_end) {
-              const double scale = __hiloint2double((E - 29 + 1023) << 20, 0);
-              v[w] = E == kNonFinite
-                         ? plain_product(a.p, w, q.e, x_row(a.p, q.t0 + i), o)
-                         : (float)((double)sum * (scale * (double)__ldg(a.p.sg[w] + q.e)));
-            }
-          }
-          if (o < o_end) write_product<NW>(a.p, v, q.t0 + i, o);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->d_empty[buf]);
+        if (!kOwnSums && ok) ok = read_sums(q, row, g, group, kGroups);
       }
     }
+    if (!ok) give_up(sh, a.status);
+  } else {
+    // ---------------------------------------------------------------- sums
+    pdl_wait();   // (for the tokens' exponents)
+    int g = 0;
+    bool ok = true;
+    while (ok && pieces.next(a, &q)) {
+      enter_pass(q);
+      for (int64_t row = q.row0; ok && row < q.row1; row += a.tile, ++g)
+        ok = read_sums(q, row, g, 0, 1);
+    }
+    if (!ok) give_up(sh, a.status);
   }
   __syncthreads();
-  if (warp == kWorkers + 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
@@ -694,8 +758,9 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
         return NVFP4_ERR_CUDA;
     }
   auto kernel = p.n_w == 2 ? product_fp4_kernel<2> : product_fp4_kernel<1>;
+  const int threads = p.n_w == 2 ? Roles<2>::kThreads : Roles<1>::kThreads;
   NVFP4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-  NVFP4_CUDA_TRY(launch_chained(kernel, dim3((unsigned)ctas), dim3(kThreads), kSmem, st, a));
+  NVFP4_CUDA_TRY(launch_chained(kernel, dim3((unsigned)ctas), dim3(threads), kSmem, st, a));
   count_launches(2);
   return NVFP4_OK;
 }

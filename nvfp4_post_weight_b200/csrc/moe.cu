@@ -5,8 +5,14 @@
 // A slot s = t * top_k + j is token t's j-th choice; `position` holds each
 // slot's row in expert order, or -1 for a slot without an expert.  Every
 // kernel but the sort goes by slots, so that a token's row is read once and
-// every sorted row is read or written by one warp: no atomics, and the result
-// does not depend on the order of the CTAs.
+// every sorted row is read or written by one warp or one column's thread: no
+// global atomics, and the result does not depend on the order of the CTAs.
+//
+// All of it is bound by DRAM bytes where there are many tokens (8192 x 8 rows of
+// 4096 bf16: the sort and the gather 107 us for 588 MB, the weighted sum 108 us
+// for 604 MB, its gradient 170 us for 1.14 GB: 5.5 to 6.7 TB/s), by launches and
+// one or two memory latencies where there are few (64 x 8: the sort 3 us, the
+// gather 2.4, the sum 2.3).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -15,6 +21,11 @@ namespace nvfp4 {
 namespace {
 
 // ---- the sort ----------------------------------------------------------------
+// Placing a warp's 32 slots in order takes about 60 cycles of its SM (the warp's
+// match and the counters), counting them by shared atomics less.  Up to 4096 slots
+// one CTA does both in one launch (512 slots: 3 us); longer inputs go over as
+// many CTAs as have 1024 slots, in three launches (65536 slots: 8 us; one CTA
+// took 125 us).
 constexpr int kSortWarps = 32;
 constexpr int kSortOneCta = 4096;   // slots that one CTA sorts by itself
 constexpr int kSortChunk = 1024;    // least slots per CTA beyond; at least NVFP4_MAX_EXPERTS
