@@ -534,3 +534,35 @@ def test_fp4_timeout_is_reported_and_the_context_survives():
     B.nvfp4_gemv(x, *w, y, ws)
     assert B.nvfp4_workspace_status(ws) == 0
     close(y, *sums_fp4(x, w))
+
+
+def test_debug_build_answers_like_the_release_build(monkeypatch):
+    """The debug build leaves out pieces of work that are not inside the call's
+    arrays; none is, so its results are the release build's, bit for bit."""
+    x = acts(40, 1024, BF16, 91)
+    w = weights((6200, 1024), 92)
+    counts = [0, 5, 1, 0, 33, 20]
+    ne = len(counts)
+    offsets = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32, device=DEV)
+    xe = acts(sum(counts), 1024, BF16, 93)
+    gate, up = weights((ne, 4352, 1024), 94), weights((ne, 4352, 1024), 95)
+    assert fp4(40, 6200, 1024) and fp4(sum(counts), 4352, 1024, ne, True)
+
+    def run():
+        y = torch.empty((40, 6200), dtype=BF16, device=DEV)
+        z = torch.empty((sum(counts), 4352), dtype=F32, device=DEV)
+        for fn, args, size in (
+                (B.nvfp4_gemv, (x, *w, y), B.nvfp4_gemv_workspace_size(40, 6200, 1024)),
+                (B.nvfp4_gemv_swiglu_experts, (xe, offsets, gate, up, z, None),
+                 B.nvfp4_gemv_workspace_size(sum(counts), 4352, 1024, ne, True))):
+            ws = B.workspace(size, DEV)
+            fn(*args, ws)
+            assert B.nvfp4_workspace_status(ws) == 0
+        return y, z
+
+    release = run()
+    monkeypatch.setattr(B, "_lib", B.debug_lib())
+    debug = run()
+    monkeypatch.undo()
+    for a, b in zip(release, debug):
+        assert torch.equal(a, b)
