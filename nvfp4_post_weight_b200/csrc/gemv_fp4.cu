@@ -19,8 +19,8 @@
 // of four warps bring the block scales to tensor memory (and read the sums).  One
 // CTA per SM streams rows of its own, equal to eight rows over all SMs, as tiles
 // of up to 128 rows (an M = 128 instruction may have rows that are not there: rows
-// do not mix), 256 or 512 columns of K a stage.  A split of K over a cluster
-// would need its sums joined; it is not needed to fill the SMs.
+// do not mix), 256 or 512 columns of K a stage.  Where few rows have many columns, two
+// CTAs share the columns: the second's sums go to the first's shared memory.
 //
 // What bounds it: one token's DRAM bytes (the 28672 x 8192 pair, 264 MB in 49.6
 // us, 82% of the copy rate); with more tokens the traffic from L2 to the SMs, where
@@ -60,6 +60,7 @@ struct Roles {
 };
 constexpr int64_t kMaxRows = 2048;                // sorted rows that are taken apart at a time
 constexpr int kTile = 128;
+constexpr int kSplitCols = 6144;                  // least columns of K that are shared out
 constexpr int kUnit = 8;                          // output columns that are shared out together
 constexpr int kSmem = 225 * 1024;
 constexpr int kTmemCols = 512;                    // sums, then buffers of a stage's scales
@@ -81,6 +82,8 @@ struct Fp4Args {
   int stage_bytes;
   int d_bufs;               // accumulators
   int sf_bufs;              // buffers of scales in tensor memory (at most ring)
+  int split;                // CTAs (one or two) that share a tile's columns of K
+  int part_bytes;           // of shared memory for the other CTA's sums
 };
 
 // ---- the tokens' digits --------------------------------------------------------
@@ -183,6 +186,7 @@ struct Shared {
   uint64_t scaled[kMaxStages];    // its scales are in tensor memory
   uint64_t empty[kMaxStages];     // its matrix instructions are done
   uint64_t d_full[2], d_empty[2]; // an accumulator is complete, has been read
+  uint64_t part_full, part_free;  // the other CTA's sums are here, have been read
   uint64_t drain;
   uint32_t tmem;
   int abort;
@@ -207,16 +211,58 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // The pipeline waits of sm100.cuh with the limit read once; given up too when
 // another role has.  Warp-wide (so that what follows stays warp-uniform and the
 // matrix instructions' operands in uniform registers).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned long long limit,
-                                     Shared* sh) {
-  bool ok = limit <= 1 ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity);
+template <typename Wait>
+__device__ __forceinline__ bool wait_by(Wait look, unsigned long long limit, Shared* sh) {
+  bool ok = look(limit <= 1);
   if (!__all_sync(0xffffffffu, ok)) {
     const uint64_t t0 = globaltimer();
     while (!ok && limit > 1 && !aborted(sh) && globaltimer() - t0 <= limit)
-      for (int i = 0; i < 16 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+      for (int i = 0; i < 16 && !ok; ++i) ok = look(false);
     ok = __all_sync(0xffffffffu, ok);
   }
   return ok;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned long long limit,
+                                     Shared* sh) {
+  return wait_by([&](bool once) { return once ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity); },
+                 limit, sh);
+}
+// The same for a barrier that the cluster's other CTA arrives at.
+__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity,
+                                             unsigned long long limit, Shared* sh) {
+  return wait_by(
+      [&](bool) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        return ok != 0;
+      },
+      limit, sh);
+}
+// This CTA's place in its cluster; the address of `p` in CTA `rank` of it.
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return (int)r;
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ bool elect() {
   uint32_t p;
@@ -287,9 +333,10 @@ struct Piece {
 };
 struct Pieces {
   int64_t u, u_end, units;
-  __device__ __forceinline__ void init(const Fp4Args& a) {
+  __device__ __forceinline__ void init(const Fp4Args& a, int split) {
     units = (a.p.d_out + kUnit - 1) / kUnit;
-    const int passes = count_passes(a.p, a.tokens), ctas = gridDim.x, b = blockIdx.x;
+    const int passes = count_passes(a.p, a.tokens), ctas = gridDim.x / split,
+              b = blockIdx.x / split;
     const int per = passes ? ctas / passes : 0;   // CTAs per pass
     if (per * passes * 16 >= ctas * 15) {
       // few passes: a whole number of CTAs each, so that no CTA has two pieces
@@ -339,19 +386,23 @@ __device__ __noinline__ float plain_product(const Product& p, int w, int e, int6
   return sum * p.sg[w][e];
 }
 
-template <int NW>
+template <int NW, int kSplit>
 __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     product_fp4_kernel(const __grid_constant__ Fp4Args a) {
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                               ~uintptr_t(1023));
+  // the other CTA's sums, the stages
+  float* part = reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                         ~uintptr_t(1023));
+  uint8_t* stages = reinterpret_cast<uint8_t*>(part) + a.part_bytes;
   __shared__ Shared shared;
   Shared* sh = &shared;
   constexpr int kSumWarp = Roles<NW>::kSumWarp, kCodeWarp = Roles<NW>::kCodeWarp,
                 kMmaWarp = Roles<NW>::kMmaWarp, kDigitWarp = Roles<NW>::kDigitWarp;
   constexpr bool kOwnSums = Roles<NW>::kOwnSums;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int P = a.panels, S = a.ring, K = a.n_stages;
+  const int P = a.panels, S = a.ring;
+  const int rank = kSplit > 1 ? cluster_rank() : 0;
+  const int k0 = a.n_stages * rank / kSplit, k1 = a.n_stages * (rank + 1) / kSplit;
   const int columns = (a.tokens + 1) / 2 * 16;   // of an accumulator, per matrix
   const int blocks = columns > 128 ? 2 : 1;      // 128-row groups of the digits' scales
   const int sf_cols = (NW + blocks) * 16 * P;    // TMEM columns of a stage's scales
@@ -375,18 +426,21 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
       mbar_init(&sh->d_empty[i], kOwnSums ? 4 : 4 * kGroups);
     }
     mbar_init(&sh->drain, 1);
+    mbar_init(&sh->part_full, kOwnSums ? 4 : 4 * kGroups);
+    mbar_init(&sh->part_free, kOwnSums ? 4 : 4 * kGroups);
     sh->abort = 0;
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tmem_alloc(&sh->tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
+  if (kSplit > 1) cluster_sync();   // (the other CTA's barriers are there)
   tc_fence_after();
   const uint32_t tmem = sh->tmem;
   const unsigned long long limit = __ldg(&g_wait_limit_ns);
 
   Pieces pieces;
-  pieces.init(a);
+  pieces.init(a, kSplit);
   Piece q;
   int s = 0;          // slot of shared memory and its phase
   uint32_t ph = 0;
@@ -417,7 +471,10 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
   auto read_sums = [&](const Piece& q, int64_t row, int g, int first, int apart) {
     const int buf = a.d_bufs == 2 ? g & 1 : 0, use = a.d_bufs == 2 ? g >> 1 : g;
     if (!wait(&sh->d_full[buf], use & 1, limit, sh)) return false;
+    if (rank > 0 && g > 0 && !wait_cluster(&sh->part_free, (g - 1) & 1, limit, sh)) return false;
+    if (rank == 0 && kSplit > 1 && !wait_cluster(&sh->part_full, g & 1, limit, sh)) return false;
     tc_fence_after();
+    const uint32_t to = rank > 0 ? cluster_addr(part, 0) : 0;
     const int64_t o = row + (threadIdx.x & (kTile - 1)), o_end = min(row + a.tile, q.row1);
     const uint32_t d = tmem + ((uint32_t)((warp & 3) * 32) << 16) + buf * NW * columns;
     // two sums at a time: both matrices' of a token, or one matrix' of two tokens
@@ -433,20 +490,31 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         float sum = c[k][7];
 #pragma unroll
         for (int p = 6; p >= 0; --p) sum = fmaf(sum, 8.f, c[k][p]);
+        const int at = (i * NW + w) * kTile + (threadIdx.x & (kTile - 1));
+        if (rank > 0) {
+          cluster_store(to + 4 * at, sum);
+          continue;
+        }
+        if (kSplit > 1) sum += part[at];
         if (o < o_end) {
           const double scale = __hiloint2double((E - 29 + 1023) << 20, 0);
           v[k] = E == kNonFinite ? plain_product(a.p, w, q.e, x_row(a.p, q.t0 + i), o)
                                  : (float)((double)sum * (scale * (double)sg[w]));
         }
       }
-      if (o < o_end) {
+      if (rank == 0 && o < o_end) {
         write_product<NW>(a.p, v, q.t0 + i0, o);
         if (NW == 1 && i0 + apart < q.n) write_product<NW>(a.p, v + 1, q.t0 + second, o);
       }
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sh->d_empty[buf]);
+    if (lane == 0) {
+      mbar_arrive(&sh->d_empty[buf]);
+      if (kSplit > 1)
+        cluster_arrive(rank ? cluster_addr(&sh->part_full, 0) : cluster_addr(&sh->part_free, 1));
+    }
+    __syncwarp();
     return true;
   };
 
@@ -464,7 +532,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         const int ops = part ? P : 1;
         const uint32_t bytes = (uint32_t)(NW * boxes * step_rows * (128 + 16) * P);
         const int y = (int)(q.e * a.p.d_out + row);
-        for (int st = 0; st < K; ++st) {
+        for (int st = k0; st < k1; ++st) {
           ok = wait(&sh->empty[s], ph ^ 1, limit, sh);
           if (!ok) break;
           uint8_t* stage = stages + s * a.stage_bytes;
@@ -499,8 +567,9 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
       const uint32_t bytes = (uint32_t)(q.n * (1024 + 16) * P);
       const int64_t next_d = a.p.n_rows * 1024, next_s = a.p.n_rows * 16;
       for (int64_t row = q.row0; ok && row < q.row1; row += a.tile) {
-        const uint8_t *d = a.digits + (int64_t)q.t0 * 1024, *f = a.sf + (int64_t)q.t0 * 16;
-        for (int st = 0; st < K; ++st) {
+        const uint8_t* d = a.digits + (int64_t)q.t0 * 1024 + k0 * P * next_d;
+        const uint8_t* f = a.sf + (int64_t)q.t0 * 16 + k0 * P * next_s;
+        for (int st = k0; st < k1; ++st) {
           ok = wait(&sh->empty[s], ph ^ 1, limit, sh);
           if (!ok) break;
           uint8_t* stage = stages + s * a.stage_bytes;
@@ -535,7 +604,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + buf * NW * columns;
         bool ready = false;
-        for (int st = 0; ok && st < K; ++st) {
+        for (int st = k0; ok && st < k1; ++st) {
           // (the group that wrote the scales has waited for the stage's copies)
           ok = ready || wait(&sh->scaled[s], ph, limit, sh);
           if (!ok) break;
@@ -543,7 +612,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
           // the next stage is looked at now: behind this one's instructions the look
           // would queue for their issue
           const int s1 = s + 1 == S ? 0 : s + 1;
-          ready = st + 1 < K && limit > 1 && mbar_test_wait(&sh->scaled[s1], s1 == 0 ? ph ^ 1 : ph);
+          ready = st + 1 < k1 && limit > 1 && mbar_test_wait(&sh->scaled[s1], s1 == 0 ? ph ^ 1 : ph);
           ready = __all_sync(0xffffffffu, ready);
           const uint32_t stage = smem_u32(stages) + s * a.stage_bytes;
           uint64_t da = smem_desc_sw128(stage, 16, 1024);
@@ -559,7 +628,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
                 for (int m = 0; m < NW; ++m)
                   mma_nvfp4(d + m * columns, da + (m * P * panel_bytes + 32 * k) / 16,
                             db + 32 * k / 16, idesc, sfa + (m * P * 4 + k) * 4, sfb + k * blocks * 4,
-                            (uint32_t)(st | p | k));
+                            (uint32_t)((st - k0) | p | k));
               da += panel_bytes / 16;
               db += columns * 128 / 16;
               sfa += 16;
@@ -608,7 +677,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     while (ok && pieces.next(a, &q)) {
       if (!kOwnSums) enter_pass(q);
       for (int64_t row = q.row0; ok && row < q.row1; row += a.tile, ++g) {
-        for (int st = 0; st < K; ++st) {
+        for (int st = k0; st < k1; ++st) {
           const int slot = s, buf = sf, no = stage_no, free_slot = os;
           const uint32_t phase = ph, free_phase = oph;
           step();
@@ -660,6 +729,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     if (!ok) give_up(sh, a.status);
   }
   __syncthreads();
+  if (kSplit > 1) cluster_sync();   // (no CTA ends while the other may still write to it)
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -720,11 +790,22 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
   const int64_t units = (p.d_out + kUnit - 1) / kUnit;
   const int64_t slots = p.offsets ? (p.n_experts < p.n_rows ? p.n_experts : p.n_rows)
                                   : (p.n_rows + a.tokens - 1) / a.tokens;
-  const int64_t ctas = units * slots < num_sms() ? units * slots : num_sms();
-  // equal tiles for the largest share of a CTA (experts': in steps of 32, see the copies)
-  const int64_t share = (units * slots + ctas - 1) / ctas * kUnit;
+  // one CTA per SM, or pairs of CTAs with half of K each: where the double share of
+  // rows is still one tile, the pair reads half the digits and is done with its chain
+  // of stages in half the time, for some 1.7 us of starting and joining (8192 x 28672,
+  // 8 tokens: 39.1 to 34.8 us, 32: 67 to 53; 6144 x 8192, 8: 18.1 to 17.2; but 8192 x
+  // 2048, 8: 10.4 to 12.0, and 9472 x 8192, whose tile would be full, 18.1 to 19.3)
+  int64_t ctas = units * slots < num_sms() ? units * slots : num_sms();
+  int64_t share = (units * slots + ctas - 1) / ctas * kUnit;   // the largest of a CTA
+  a.split = 2 * share < kTile && p.d_in >= kSplitCols ? 2 : 1;
+  if (a.split == 2) {
+    ctas = units * slots < num_sms() / 2 ? units * slots : num_sms() / 2;
+    share = (units * slots + ctas - 1) / ctas * kUnit;
+  }
+  // equal tiles for it (experts': in steps of 32, see the copies)
   const int64_t tiles = (share + kTile - 1) / kTile, grain = p.offsets ? 32 : kUnit;
   a.tile = (int)(((share + tiles - 1) / tiles + grain - 1) / grain * grain);
+  a.part_bytes = a.split > 1 ? (a.tokens * p.n_w * kTile * 4 + 1023) / 1024 * 1024 : 0;
   // panels per stage: two (a stage costs each role a few hundred cycles whatever its
   // size) where that leaves a ring of three stages, or four for two matrices
   for (a.panels = kMaxPanels; a.panels >= 1; a.panels /= 2) {
@@ -733,7 +814,7 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
                      32 * 16 + 1023) / 1024 * 1024;
     // (rows that a tile lacks are read behind the last stage too)
     const int behind = (kTile - a.tile) * (128 + 16 * a.panels);
-    a.ring = (kSmem - 1024 - behind) / a.stage_bytes;
+    a.ring = (kSmem - 1024 - behind - a.part_bytes) / a.stage_bytes;
     const int sf_cols = (p.n_w + (columns > 128 ? 2 : 1)) * 16 * a.panels;
     a.d_bufs = 2 * p.n_w * columns + 2 * sf_cols <= kTmemCols ? 2 : 1;
     a.sf_bufs = (kTmemCols - a.d_bufs * p.n_w * columns) / sf_cols;
@@ -757,10 +838,25 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
                           CU_TENSOR_MAP_SWIZZLE_NONE))
         return NVFP4_ERR_CUDA;
     }
-  auto kernel = p.n_w == 2 ? product_fp4_kernel<2> : product_fp4_kernel<1>;
+  auto kernel = a.split == 2 ? (p.n_w == 2 ? product_fp4_kernel<2, 2> : product_fp4_kernel<1, 2>)
+                             : (p.n_w == 2 ? product_fp4_kernel<2, 1> : product_fp4_kernel<1, 1>);
   const int threads = p.n_w == 2 ? Roles<2>::kThreads : Roles<1>::kThreads;
   NVFP4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
-  NVFP4_CUDA_TRY(launch_chained(kernel, dim3((unsigned)ctas), dim3(threads), kSmem, st, a));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas * a.split));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.split > 1 ? 2 : 1;
+  NVFP4_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a));
   count_launches(2);
   return NVFP4_OK;
 }
