@@ -350,21 +350,46 @@ nvfp4_status launch_kernel(const Args& a, dim3 grid, int S, size_t smem, cudaStr
   return NVFP4_OK;
 }
 
+// How the general kernel divides its work.  The size of the workspace goes by it too,
+// so that it depends on sizes alone: no addresses, and a B200's SMs whether a device
+// is there or not (one with other SMs gets the same, right division).
+constexpr int kSms = 148;
+struct Division {
+  int64_t tiles, slots;   // of output columns; experts that may have rows
+  int n_chunks, slices;   // of K
+  int nt;                 // eights of tokens per pass: the rows of one expert on average
+  int64_t wave;           // CTAs that run at a time
+};
+
+// Slices of K, each of two chunks at least: as many as leave the CTAs one wave; beyond
+// it to four where the wave would be less than two thirds full.  8192 x 8192, one
+// token: 4 slices 15.2 us, 8 (1.7 waves) 18.1; 12288 x 8192: 4 slices (1.3 waves) 23.5,
+// 2 (0.65) 26.1.  (5, 6 and 7 slices, whose clusters fill the SMs unevenly, take
+// longer than 4 and 8.)
+Division divide(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, int n_w) {
+  Division v;
+  v.tiles = (d_out + kRowsCta - 1) / kRowsCta;
+  v.slots = n_experts == 0 ? 1 : n_experts < n_rows ? n_experts : n_rows;
+  v.n_chunks = (int)((d_in + kChunk - 1) / kChunk);
+  const int64_t mean = (n_rows + v.slots - 1) / v.slots, work = v.tiles * v.slots;
+  v.nt = mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
+  v.wave = (v.nt * n_w > 4 ? 1 : 2) * kSms;   // (the kernel's launch bounds)
+  v.slices = 1;
+  while (v.slices < 8 && v.n_chunks >= 4 * v.slices &&
+         (2 * v.slices * work <= v.wave || (v.slices < 4 && 3 * v.slices * work < 2 * v.wave)))
+    v.slices *= 2;
+  return v;
+}
+
 nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
   Args a{};
   a.p = p;
   a.status = status;
   const bool glu = p.n_w == 2;
-  const int64_t tiles = (p.d_out + kRowsCta - 1) / kRowsCta;
-  const int64_t slots = !p.offsets ? 1 : p.n_experts < p.n_rows ? p.n_experts : p.n_rows;
-  const int n_chunks = (int)((p.d_in + kChunk - 1) / kChunk);
-  // slices of K: until the CTAs fill the GPU (two an SM), each of two chunks at least
-  int S = 1;
-  while (S < 8 && tiles * slots * S < 2 * num_sms() && n_chunks >= 4 * S) S *= 2;
+  const Division v = divide(p.n_rows, p.d_out, p.d_in, p.offsets ? p.n_experts : 0, p.n_w);
+  const int64_t tiles = v.tiles, slots = v.slots;
+  const int n_chunks = v.n_chunks, S = v.slices, nt = v.nt;
   a.slice = (n_chunks + S - 1) / S;
-  // tokens per pass: the rows of one expert on average
-  const int64_t mean = (p.n_rows + slots - 1) / slots;
-  const int nt = mean <= 8 ? 1 : mean <= 16 ? 2 : 4;
   const int64_t tok = p.n_rows < 8 * nt ? p.n_rows : 8 * nt;
   const int planes = p.x_bf16 ? 1 : 3;
   const int64_t per_chunk = planes * tok * 256;
@@ -405,24 +430,35 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
   return s;
 }
 
-// Whether the FP4 path is the faster one.  Its CTAs walk all of K one after
-// another (some 0.25 us per 256 columns) however few rows they have, where this
-// kernel also slices K; measured, us, FP4 / this kernel, one token and 32:
-// 1024 x 8192: 14.7 / 6.5 and 24.6 / 16.6; 8192 x 8192: 17.2 / 20.9 and 26.2 /
-// 40.9; 8192 x 2048: 8.6 / 8.8 and 13.3 / 15.9; 1024 x 512: 6.7 / 7.1 and 10.3 /
-// 14.5.  By expert it also has to find its rows, so the bytes of the experts'
-// codes decide, the more rows they have the sooner: 32 experts of 768 x 2048
-// (25 MB), one row each 13.3 / 11.0, four 20.5 / 25.0; 8 pairs of 1536 x 4096
-// (50 MB), one row each 20.2 / 25.2.  No addresses: the workspace goes by it too.
-// n_experts 0: one matrix or pair.
+// Whether the FP4 path is the faster one.  It starts with a launch of its own and walks
+// all of K, or half, one stage after another, however few rows a CTA has; the general
+// kernel slices K further, but decodes.  So for one matrix or pair both are estimated,
+// in columns of K that the general kernel decodes: its CTA's slice with some 300 for
+// each start, times what more tokens cost it, less where its CTAs do not fill the SMs,
+// against 1100 and a sixth of K or, from 32 tokens on, four tenths.  Measured, us, FP4
+// / general, one token and 32: 1024 x 8192: 14.7 / 6.5 and 24.6 / 16.6; 8192 x 2048:
+// 8.9 / 6.8 and 15.3 / 14.2; 8192 x 8192: 16.7 / 15.4 and 26.9 / 35.1; 4096 x 28672:
+// 26.0 / 23.3; 5120 x 12288: 18.0 / 20.7 and 31.4 / 48.1; 10240 x 8192: 17.5 / 23.3 and
+// 30.7 / 56.0; the pair of 4096 x 8192: 17.6 / 15.6 and 22.8 / 33.4.
+// By expert it also has to find its rows, so the bytes of the experts' codes decide,
+// the more rows they have the sooner: 32 experts of 768 x 2048 (25 MB), one row each
+// 13.3 / 11.0, four 20.5 / 25.0; 8 pairs of 1536 x 4096 (50 MB), one row each 19.6 /
+// 25.1.  n_experts 0: one matrix or pair.
 bool fp4_path(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, int n_w,
               nvfp4_dtype xt) {
   if (xt != NVFP4_BF16 || !product_fp4_shape(n_rows, d_in)) return false;
+  const Division v = divide(n_rows, d_out, d_in, n_experts, n_w);
   if (n_experts > 0) {
-    const int64_t slots = n_experts < n_rows ? n_experts : n_rows, mean = n_rows / slots;
-    return n_w * slots * d_out * d_in / 2 * (mean < 4 ? mean : 4) >= 48000000;
+    const int64_t mean = n_rows / v.slots;
+    return n_w * v.slots * d_out * d_in / 2 * (mean < 4 ? mean : 4) >= 48000000;
   }
-  return d_out >= 6144 || d_in <= 1024;
+  const int64_t ctas = v.tiles * v.slices;
+  const double waves = (double)((ctas + v.wave - 1) / v.wave);
+  const double decode = v.nt == 1 ? 1. : v.nt == 2 ? 1.5 : 2.6 * (double)((n_rows + 31) / 32);
+  double general = waves * ((double)d_in / v.slices * n_w * decode + 300.);
+  if (ctas < kSms) general *= 0.5 + 0.5 * (double)ctas / kSms;
+  const double more = n_rows <= 8 ? 0. : (double)((n_rows < 32 ? n_rows : 32) - 8);
+  return general >= 1100. + (0.17 + 0.01 * more) * (double)d_in;
 }
 
 constexpr int64_t kMaxDim = 1 << 17, kMaxRows = 1 << 22;

@@ -362,11 +362,15 @@ def gated_fp4(x, gate, up):
 
 
 @pytest.mark.parametrize("n_tok", [1, 2, 7, 8, 16, 17, 24, 25, 32, 33, 70])
-@pytest.mark.parametrize("d_out,d_in", [(6144, 2048), (7001, 512), (30000, 256), (40, 768), (8, 256)])
+@pytest.mark.parametrize("d_out,d_in", [(6144, 2048), (7001, 512), (30000, 256), (40, 768), (8, 256),
+                                        (10301, 2304), (150001, 256), (80000, 768), (5201, 12544),
+                                        (40, 28672)])
 def test_gemv_fp4(n_tok, d_out, d_in):
     """One and several passes over the tokens, one and several tiles a CTA, rows
-    that end inside a unit, one panel and several."""
-    assert fp4(n_tok, d_out, d_in)
+    that end inside a unit, one panel and several, K in one part and in two (5201,
+    and 40 for 70 tokens).  (The smaller ones run on either kernel.)"""
+    assert fp4(n_tok, d_out, d_in) or d_out * d_in < 2 ** 24
+    assert not fp4(1, 40, d_in)
     w = weights((d_out, d_in), d_out + d_in)
     for xt, yt in ((BF16, F32), (F32, BF16), (BF16, BF16), (F32, F32)):
         x = acts(n_tok, d_in, xt, n_tok)
@@ -376,9 +380,10 @@ def test_gemv_fp4(n_tok, d_out, d_in):
 
 
 @pytest.mark.parametrize("n_tok", [1, 5, 24, 25, 49])
-@pytest.mark.parametrize("d_out,d_in", [(6144, 1024), (20011, 256), (100, 512)])
+@pytest.mark.parametrize("d_out,d_in", [(6144, 1024), (20011, 256), (100, 512),
+                                        (9505, 2048), (100003, 256), (2605, 12544)])
 def test_gemv_swiglu_fp4(n_tok, d_out, d_in):
-    assert fp4(n_tok, d_out, d_in, 0, True)
+    assert fp4(n_tok, d_out, d_in, 0, True) or d_out * d_in < 2 ** 24
     gate, up = weights((d_out, d_in), 1 + d_in), weights((d_out, d_in), 2 + d_in)
     for xt in (BF16, F32):
         x = acts(n_tok, d_in, xt, n_tok) * 0.1
@@ -387,11 +392,12 @@ def test_gemv_swiglu_fp4(n_tok, d_out, d_in):
         close(y, *gated_fp4(x, gate, up))
 
 
-def test_fp4_bf16_entries_near_their_block_are_exact():
+@pytest.mark.parametrize("times", [1, 600])
+def test_fp4_bf16_entries_near_their_block_are_exact(times):
     """Entries within 2^-14 of their block's largest lose nothing: one nonzero
     weight a column picks single entries out exactly."""
     d_in = d_out = 256
-    assert fp4(4, d_out, d_in)
+    assert fp4(4, d_out * times, d_in) == (times > 1)
     g = torch.Generator().manual_seed(1)
     x = (torch.rand((4, d_in), generator=g) + 1) * 2.0 ** -torch.randint(0, 14, (4, d_in), generator=g)
     x = (x * (torch.randint(0, 2, (4, d_in), generator=g) * 2 - 1)).to(BF16).to(DEV)
@@ -400,14 +406,16 @@ def test_fp4_bf16_entries_near_their_block_are_exact():
     codes[torch.arange(d_out), torch.arange(d_in)] = 2          # 1.0
     packed = (codes[:, 0::2] | codes[:, 1::2] << 4).to(DEV)
     scales = torch.full((d_out, d_in // 16), 56, dtype=torch.uint8, device=DEV)   # 1.0
-    y = torch.empty((4, d_out), device=DEV)
-    B.nvfp4_gemv(x, packed, scales, torch.ones(1, device=DEV), y)
-    assert torch.equal(y, x.float())
+    y = torch.empty((4, d_out * times), device=DEV)
+    B.nvfp4_gemv(x, packed.repeat(times, 1), scales.repeat(times, 1), torch.ones(1, device=DEV), y)
+    assert torch.equal(y, x.float().repeat(1, times))
 
 
+@pytest.mark.parametrize("d_out", [6200, 40003])
 @pytest.mark.parametrize("xt", [BF16, F32])
-def test_fp4_extreme_and_nonfinite_tokens(xt):
-    d_in, d_out = 512, 6200
+def test_fp4_extreme_and_nonfinite_tokens(xt, d_out):
+    d_in = 512
+    assert fp4(9, d_out, d_in) == (d_out > 6200)
     w = weights((d_out, d_in), 3)
     x = acts(9, d_in, F32, 4)
     x[1] *= 1e30
@@ -479,7 +487,8 @@ def test_fp4_bad_offsets_are_cut():
 
 def test_fp4_unaligned_bases_run_elsewhere():
     """Codes 8 bytes or scales one byte off a 16-byte boundary: same answer."""
-    d_out, d_in = 300, 512
+    d_out, d_in = 40003, 512
+    assert fp4(3, d_out, d_in)
     w, x = weights((d_out, d_in), 8), acts(3, d_in, BF16, 2)
     codes = torch.empty(w[0].numel() + 8, dtype=torch.uint8, device=DEV)[8:].view(w[0].shape)
     scales = torch.empty(w[1].numel() + 1, dtype=torch.uint8, device=DEV)[1:].view(w[1].shape)
@@ -495,7 +504,8 @@ def test_fp4_unaligned_bases_run_elsewhere():
 
 
 def test_fp4_same_bits_on_streams_and_in_graphs():
-    d_out, d_in = 6500, 1024
+    d_out, d_in = 20003, 1024
+    assert fp4(6, d_out, d_in)
     w, x = weights((d_out, d_in), 31), acts(6, d_in, BF16, 3)
     y, z, v = (torch.empty((6, d_out), device=DEV) for _ in range(3))
     ws = [B.workspace(B.nvfp4_gemv_workspace_size(6, d_out, d_in), DEV) for _ in range(2)]
@@ -516,10 +526,11 @@ def test_fp4_same_bits_on_streams_and_in_graphs():
     assert torch.equal(y, z) and torch.equal(y, v)
 
 
-def test_fp4_timeout_is_reported_and_the_context_survives():
+@pytest.mark.parametrize("d_out,d_in", [(20003, 1024), (5201, 12544)])
+def test_fp4_timeout_is_reported_and_the_context_survives(d_out, d_in):
     """With a wait limit of 1 ns every wait of the kernel gives up: the status
     says so, and the next call is right again."""
-    d_out, d_in = 7000, 1024
+    assert fp4(5, d_out, d_in)
     w, x = weights((d_out, d_in), 5), acts(5, d_in, BF16, 3)
     y = torch.zeros((5, d_out), device=DEV)
     ws = B.workspace(B.nvfp4_gemv_workspace_size(5, d_out, d_in), DEV)

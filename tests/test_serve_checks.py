@@ -42,13 +42,15 @@ def test_gemv_swiglu_refuses():
 
 
 def test_gemv_refuses_a_missing_or_small_workspace():
-    need = B.nvfp4_gemv_workspace_size(3, 16, 512)
-    assert need > 3 * 512 * 4 and B.nvfp4_gemv_workspace_size(3, 16, 32) == 0
-    assert B.lib().nvfp4_gemv_workspace_size(-1, 16, 512, 0, 0, 0) == 0
-    assert B.nvfp4_gemv_workspace_size(3, 16, 512, dtype=torch.float32) == 0
+    o = 40003
+    need = B.nvfp4_gemv_workspace_size(3, o, 512)
+    assert need > 3 * 512 * 4 and B.nvfp4_gemv_workspace_size(3, 16, 512) == 0
+    assert B.nvfp4_gemv_workspace_size(3, o, 528) == 0
+    assert B.lib().nvfp4_gemv_workspace_size(-1, o, 512, 0, 0, 0) == 0
+    assert B.nvfp4_gemv_workspace_size(3, o, 512, dtype=torch.float32) == 0
     for kw in (dict(), dict(ws=A, nws=need - 1), dict(ws=P(128), nws=need)):
-        assert gemv(n=3, i=512, **kw) == 3
-    assert gemv(n=0, i=512) == OK
+        assert gemv(n=3, o=o, i=512, **kw) == 3
+    assert gemv(n=0, o=o, i=512) == OK
 
 
 @pytest.mark.parametrize("kw,status", [
