@@ -8,11 +8,11 @@
 // every sorted row is read or written by one warp or one column's thread: no
 // global atomics, and the result does not depend on the order of the CTAs.
 //
-// All of it is bound by DRAM bytes where there are many tokens (8192 x 8 rows of
-// 4096 bf16: the sort and the gather 107 us for 588 MB, the weighted sum 108 us
-// for 604 MB, its gradient 170 us for 1.14 GB: 5.5 to 6.7 TB/s), by launches and
-// one or two memory latencies where there are few (64 x 8: the sort 3 us, the
-// gather 2.4, the sum 2.3).
+// All of it is bound by DRAM bytes where there are many tokens (8192 x 8 slots, 3%
+// of them empty, rows of 4096 bf16: the sort 8 us, the gather 99 us and the weighted
+// sum 88 us for 587 MB each, its gradient 170 us for 1.11 GB: 5.9 to 6.7 TB/s), by
+// launches and one or two memory latencies where there are few (64 x 8: the sort 3
+// us, the gather 2.4, the sum 2.4).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -280,6 +280,29 @@ __device__ __forceinline__ int64_t first_column(int64_t b, int t, int threads) {
 __device__ __forceinline__ float as_f32(float v) { return v; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 
+// V elements of a row, held until they are used.  Of one access: as 32-bit words (as
+// arrays of bf16 they do not stay in registers: 8192 x 8 rows of 4096 took 108 us to
+// add up, 88 us so).
+template <typename T, int V, bool kVec>
+struct alignas(sizeof(T) * V) Held {
+  uint32_t w[V * sizeof(T) / 4];
+  __device__ __forceinline__ void load(const T* row, int64_t c, int64_t) {
+    *this = *reinterpret_cast<const Held*>(row + c);
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+    return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+  }
+};
+template <typename T, int V>
+struct Held<T, V, false> {
+  T v[V];
+  __device__ __forceinline__ void load(const T* row, int64_t c, int64_t d) {
+    load_row<T, V, false, 256>(row, c, d, v);
+  }
+  __device__ __forceinline__ float operator[](int i) const { return as_f32(v[i]); }
+};
+
 // Token blockIdx.x's row to the sorted rows of its slots: one read, top_k writes.
 template <typename T, int V, bool kVec>
 __global__ void __launch_bounds__(256)
@@ -312,19 +335,20 @@ __global__ void __launch_bounds__(256)
     float acc[V] = {};
     for (int j0 = 0; j0 < top_k; j0 += kAhead) {
       int64_t p[kAhead];
-      alignas(16) TS y[kAhead][V];
+      Held<TS, V, kVec> y[kAhead];
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         p[j] = j0 + j < top_k ? position[t * top_k + j0 + j] : -1;
         if (p[j] >= n_slots) p[j] = -1;
-        if (p[j] >= 0) load_row<TS, V, kVec, 256>(Ys + p[j] * d, c, d, y[j]);
+        if (kVec) y[j] = {};   // (else the loads wait for the positions: 92 us)
+        if (p[j] >= 0) y[j].load(Ys + p[j] * d, c, d);
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         if (p[j] < 0) continue;
         const float w = weights ? weights[t * top_k + j0 + j] : 1.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] = fmaf(w, as_f32(y[j][i]), acc[i]);
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(w, y[j][i], acc[i]);
       }
     }
     alignas(16) TY o[V];
