@@ -635,6 +635,8 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
+
+
 # (these calls may take a few microseconds on the device, so their checks first
 # ask what holds for good arguments and leave the message to _need)
 def _arg(call, t, name, shape, dtype, dev):
@@ -653,14 +655,32 @@ def _arg(call, t, name, shape, dtype, dev):
     return t.data_ptr()
 
 
-def _io_matrix(call, t, name):
-    """(rows, columns, library dtype, device number) of a contiguous bf16 or
-    fp32 CUDA matrix."""
-    if (type(t) is torch.Tensor and t.is_cuda and t.dim() == 2 and t.dtype in _IO_DTYPES
-            and t.is_contiguous()):
-        return *t.shape, NVFP4_BF16 if t.dtype is torch.bfloat16 else NVFP4_F32, t.get_device()
-    rows, cols = _matrix(call, t, name, _IO_DTYPES)
-    return rows, cols, _dtype_code(t), t.get_device()
+_IO_CODES = {torch.bfloat16: NVFP4_BF16, torch.float32: NVFP4_F32}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _io_matrix(call, t, name, codes=_IO_CODES):
+    """(rows, columns, library dtype, device number) of a contiguous CUDA matrix
+    of one of the dtypes of codes (bf16 and fp32)."""
+    if (type(t) is not torch.Tensor or not t.is_cuda or t.dim() != 2 or t.dtype not in codes
+            or not t.is_contiguous()):
+        _matrix(call, t, name, tuple(codes))
+    return *t.shape, codes[t.dtype], t.get_device()
+
+
+def _sorted_rows(call, t, name, shape, dev):
+    """(pointer, library dtype) of a bf16 or fp32 matrix of the given shape."""
+    if type(t) is not torch.Tensor or t.dtype not in _IO_CODES:
+        _matrix(call, t, name, _IO_DTYPES)
+    return _arg(call, t, name, shape, t.dtype, dev), _IO_CODES[t.dtype]
+
+
+def _offsets(call, t, dev):
+    """(pointer, number of experts) of offsets (experts + 1,)."""
+    if type(t) is not torch.Tensor or t.dim() != 1 or not t.numel():
+        _need(call, t, "offsets", dtype=_I32, numel_min=1)
+    n = t.numel()
+    return _arg(call, t, "offsets", (n,), _I32, dev), n - 1
 
 
 def _run_on(call, dev, stream, *args):
@@ -717,11 +737,10 @@ def _product(call, X, weights, Y, offsets, rows, ws, stream):
     if offsets is None:
         lead, head = (), ()
     else:
-        _need(call, offsets, "offsets", dtype=_I32, numel_min=1)
-        n = offsets.numel()
+        pointer, experts = _offsets(call, offsets, dev)
         head = (None if rows is None else _arg(call, rows, "rows", (n_rows,), _I32, dev),
-                _arg(call, offsets, "offsets", (n,), _I32, dev), n - 1, n_rows)
-        lead = (n - 1,)
+                pointer, experts, n_rows)
+        lead = (experts,)
     w = []
     for name, t in weights:
         w += _weight(call, name, t, lead, d_out, d_in, dev)
@@ -759,16 +778,18 @@ def nvfp4_gemv_experts(X, offsets, codes, scales, global_scales, Y, rows=None, w
     scales (experts, d_out, d_in/16), global_scales (experts,).  Rows outside
     every expert are left as they were."""
     call = "nvfp4_gemv_experts"
-    _product(call, X, [("", (codes, scales, global_scales))], Y, _need(call, offsets, "offsets"),
-             rows, ws, stream)
+    if offsets is None:
+        _need(call, offsets, "offsets")
+    _product(call, X, [("", (codes, scales, global_scales))], Y, offsets, rows, ws, stream)
 
 
 def nvfp4_gemv_swiglu_experts(X, offsets, gate, up, Y, rows=None, ws=None, stream=None):
     """nvfp4_gemv_swiglu by expert; gate, up: (codes, scales, global_scales)
     stacked as for nvfp4_gemv_experts."""
     call = "nvfp4_gemv_swiglu_experts"
-    _product(call, X, [("gate ", gate), ("up ", up)], Y, _need(call, offsets, "offsets"), rows, ws,
-             stream)
+    if offsets is None:
+        _need(call, offsets, "offsets")
+    _product(call, X, [("gate ", gate), ("up ", up)], Y, offsets, rows, ws, stream)
 
 
 def on_stream(stream):
@@ -791,11 +812,9 @@ def nvfp4_moe_sort(expert_ids, offsets, rows, position, stream=None):
     (n_tok * top_k,) and position (n_tok, top_k), all int32: the slots in a
     stable order by expert; ids outside 0..experts-1 have no row (-1)."""
     call = "nvfp4_moe_sort"
-    n_tok, top_k = _matrix(call, expert_ids, "expert_ids", (_I32, torch.int64))
-    _need(call, offsets, "offsets", dtype=_I32, numel_min=1)
-    dev, n = expert_ids.get_device(), offsets.numel()
-    _run_on(call, dev, stream, expert_ids.data_ptr(), expert_ids.element_size(), n_tok, top_k,
-            n - 1, _arg(call, offsets, "offsets", (n,), _I32, dev),
+    n_tok, top_k, id_bytes, dev = _io_matrix(call, expert_ids, "expert_ids", _ID_BYTES)
+    pointer, experts = _offsets(call, offsets, dev)
+    _run_on(call, dev, stream, expert_ids.data_ptr(), id_bytes, n_tok, top_k, experts, pointer,
             _arg(call, rows, "rows", (n_tok * top_k,), _I32, dev),
             _arg(call, position, "position", (n_tok, top_k), _I32, dev))
 
@@ -823,8 +842,8 @@ def nvfp4_moe_combine(Ys, position, Y, weights=None, stream=None):
     call = "nvfp4_moe_combine"
     n_tok, d, yt, dev = _io_matrix(call, Y, "Y")
     pos, top_k = _slots(call, position, n_tok, dev)
-    _, _, st, _ = _io_matrix(call, Ys, "Ys")
-    _run_on(call, dev, stream, _arg(call, Ys, "Ys", (n_tok * top_k, d), Ys.dtype, dev), st, pos,
+    rows, st = _sorted_rows(call, Ys, "Ys", (n_tok * top_k, d), dev)
+    _run_on(call, dev, stream, rows, st, pos,
             None if weights is None else _arg(call, weights, "weights", (n_tok, top_k), _F32, dev),
             n_tok, top_k, d, Y.data_ptr(), yt)
 
