@@ -635,8 +635,6 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                               lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-
-
 # (these calls may take a few microseconds on the device, so their checks first
 # ask what holds for good arguments and leave the message to _need)
 def _arg(call, t, name, shape, dtype, dev):
