@@ -498,7 +498,9 @@ nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const
 
 /* Bytes of workspace of the products: n_rows rows of Y (n_tok, or the experts
  * forms' n_rows), the matrices' sizes, the experts forms' n_experts (0 for the
- * others), pair: 1 for the swiglu forms, X's type. */
+ * others), pair: 1 for the swiglu forms, X's type.  A size that the FP4 path
+ * takes needs one and its neighbours may not: ask for each n_rows that is
+ * used, the largest answer serves them all.  0 for sizes that a call refuses. */
 size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts,
                                  int pair, nvfp4_dtype x_dtype);
 

@@ -30,6 +30,7 @@
 // form with the codes copied to shared memory (77 us for the pair, but 708 us
 // where this takes 305: 64 tokens' rows through 128 experts' pairs).
 #include <cooperative_groups.h>
+#include <math.h>
 
 #include "gemv.cuh"
 
@@ -441,16 +442,17 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
 // 26.0 / 23.3; 5120 x 12288: 18.0 / 20.7 and 31.4 / 48.1; 10240 x 8192: 17.5 / 23.3 and
 // 30.7 / 56.0; the pair of 4096 x 8192: 17.6 / 15.6 and 22.8 / 33.4.
 // By expert it also has to find its rows, so the bytes of the experts' codes decide,
-// the more rows they have the sooner: 32 experts of 768 x 2048 (25 MB), one row each
-// 13.3 / 11.0, four 20.5 / 25.0; 8 pairs of 1536 x 4096 (50 MB), one row each 19.6 /
-// 25.1.  n_experts 0: one matrix or pair.
+// the more rows they have the sooner: 8 pairs of 768 x 2048 (13 MB), 4, 16 and 64 rows
+// each 14.2 / 11.6, 16.9 / 15.1 and 39.9 / 52.6; 8 of 4096 x 1536 (25 MB), one row and 16
+// each 15.6 / 13.6 and 19.3 / 21.8; 8 pairs of 1536 x 4096 (50 MB), one row each 19.7 /
+// 25.2.  n_experts 0: one matrix or pair.
 bool fp4_path(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, int n_w,
               nvfp4_dtype xt) {
   if (xt != NVFP4_BF16 || !product_fp4_shape(n_rows, d_in)) return false;
   const Division v = divide(n_rows, d_out, d_in, n_experts, n_w);
   if (n_experts > 0) {
-    const int64_t mean = n_rows / v.slots;
-    return n_w * v.slots * d_out * d_in / 2 * (mean < 4 ? mean : 4) >= 48000000;
+    const double bytes = (double)(n_w * v.slots) * (double)d_out * (double)d_in / 2;
+    return bytes * cbrt((double)(n_rows / v.slots)) >= 40e6;
   }
   const int64_t ctas = v.tiles * v.slices;
   const double waves = (double)((ctas + v.wave - 1) / v.wave);
@@ -529,7 +531,8 @@ extern "C" {
 
 size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts,
                                  int pair, nvfp4_dtype x_dtype) {
-  if (n_rows < 0 || d_out < 0 || n_experts < 0 ||
+  if (n_rows < 0 || d_out < 0 || n_experts < 0 || d_out > kMaxRows || d_in > kMaxDim ||
+      n_experts > NVFP4_MAX_EXPERTS ||
       !fp4_path(n_rows, d_out, d_in, n_experts, pair ? 2 : 1, x_dtype))
     return 0;
   return product_fp4_ws_bytes(n_rows, d_in);

@@ -46,6 +46,8 @@ def test_gemv_refuses_a_missing_or_small_workspace():
     need = B.nvfp4_gemv_workspace_size(3, o, 512)
     assert need > 3 * 512 * 4 and B.nvfp4_gemv_workspace_size(3, 16, 512) == 0
     assert B.nvfp4_gemv_workspace_size(3, o, 528) == 0
+    assert B.nvfp4_gemv_workspace_size(3, o, 1 << 40) == 0
+    assert B.nvfp4_gemv_workspace_size(3, 1 << 40, 512) == 0
     assert B.lib().nvfp4_gemv_workspace_size(-1, o, 512, 0, 0, 0) == 0
     assert B.nvfp4_gemv_workspace_size(3, o, 512, dtype=torch.float32) == 0
     for kw in (dict(), dict(ws=A, nws=need - 1), dict(ws=P(128), nws=need)):
