@@ -22,7 +22,7 @@
 // This kernel takes what the FP4 path (gemv_fp4.cu) does not: fp32 tokens, rows
 // that are not whole panels of 256 columns, other alignments, and sizes that are
 // over before that path's chain of stages is.  What bounds it there is latency
-// (1024 x 8192, one token: 4.7 MB in 6.5 us, of which a launch, a DRAM access, the
+// (1024 x 8192, one token: 4.7 MB in 6.2 us, of which a launch, a DRAM access, the
 // staging of the tokens and the join take five); with more weights the issue of
 // some 3.7 instructions per weight (the 28672 x 8192 pair: 86 us).  fp16 operands
 // by the e2m1 conversion instruction needed 2.5 per weight and took longer (94
@@ -335,6 +335,9 @@ nvfp4_status launch_kernel(const Args& a, dim3 grid, int S, size_t smem, cudaStr
   if (smem > 48 * 1024)
     NVFP4_CUDA_TRY(
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  if (S > 8)
+    NVFP4_CUDA_TRY(
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(32 * kWarps);
@@ -366,7 +369,10 @@ struct Division {
 // it to four where the wave would be less than two thirds full.  8192 x 8192, one
 // token: 4 slices 15.2 us, 8 (1.7 waves) 18.1; 12288 x 8192: 4 slices (1.3 waves) 23.5,
 // 2 (0.65) 26.1.  (5, 6 and 7 slices, whose clusters fill the SMs unevenly, take
-// longer than 4 and 8.)
+// longer than 4 and 8.)  Sixteen, a cluster that needs leave and joins more slowly,
+// where that still leaves an SM to each CTA and three chunks a slice: 1024 x 8192, one
+// token 6.5 to 6.2 us, 512 x 8192 6.5 to 5.1, 256 x 16384 9.2 to 6.6; but 1000 x 4112, 5
+// fp32 tokens (33 chunks) 8.0 to 8.4.
 Division divide(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, int n_w) {
   Division v;
   v.tiles = (d_out + kRowsCta - 1) / kRowsCta;
@@ -379,6 +385,7 @@ Division divide(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, 
   while (v.slices < 8 && v.n_chunks >= 4 * v.slices &&
          (2 * v.slices * work <= v.wave || (v.slices < 4 && 3 * v.slices * work < 2 * v.wave)))
     v.slices *= 2;
+  if (v.slices == 8 && 16 * work <= kSms && v.n_chunks >= 48 && v.wave > kSms) v.slices = 16;
   return v;
 }
 
@@ -437,7 +444,7 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
 // in columns of K that the general kernel decodes: its CTA's slice with some 300 for
 // each start, times what more tokens cost it, less where its CTAs do not fill the SMs,
 // against 1100 and a sixth of K or, from 32 tokens on, four tenths.  Measured, us, FP4
-// / general, one token and 32: 1024 x 8192: 14.7 / 6.5 and 24.6 / 16.6; 8192 x 2048:
+// / general, one token and 32: 1024 x 8192: 14.7 / 6.2 and 24.6 / 13.6; 8192 x 2048:
 // 8.9 / 6.8 and 15.3 / 14.2; 8192 x 8192: 16.7 / 15.4 and 26.9 / 35.1; 4096 x 28672:
 // 26.0 / 23.3; 5120 x 12288: 18.0 / 20.7 and 31.4 / 48.1; 10240 x 8192: 17.5 / 23.3 and
 // 30.7 / 56.0; the pair of 4096 x 8192: 17.6 / 15.6 and 22.8 / 33.4.

@@ -577,3 +577,29 @@ def test_debug_build_answers_like_the_release_build(monkeypatch):
     monkeypatch.undo()
     for a, b in zip(release, debug):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("d_out,d_in", [(1, 6016), (130, 6160), (1100, 8192), (130, 131072)])
+@pytest.mark.parametrize("n_tok", [1, 9, 40])
+def test_gemv_of_few_columns_and_long_rows(n_tok, d_out, d_in):
+    """K in sixteen slices, some of them short."""
+    w = weights((d_out, d_in), d_out + d_in)
+    for xt, yt in ((BF16, F32), (F32, F32)):
+        x = acts(n_tok, d_in, xt, n_tok)
+        y = torch.full((n_tok, d_out), 7.0, dtype=yt, device=DEV)
+        B.nvfp4_gemv(x, *w, y)
+        close(y, *(sums_fp4 if xt == BF16 else sums)(x, w))
+
+
+def test_swiglu_and_experts_of_few_columns_and_long_rows():
+    gate, up = (weights((130, 8192), s) for s in (3, 4))
+    x = acts(11, 8192, BF16, 5) * 0.1
+    y = torch.full((11, 130), 7.0, device=DEV)
+    B.nvfp4_gemv_swiglu(x, gate, up, y)
+    close(y, *gated_fp4(x, gate, up))
+    w = weights((3, 130, 8192), 6)
+    offsets = torch.tensor([1, 1, 4, 7], dtype=torch.int32, device=DEV)
+    z = torch.full((11, 130), 7.0, device=DEV)
+    B.nvfp4_gemv_experts(x, offsets, *w, z)
+    by_expert(lambda r, *m: close(z[r], *sums_fp4(x[r], *m)), offsets, w)
+    assert (z[0] == 7).all() and (z[7:] == 7).all()
