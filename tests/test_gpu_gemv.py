@@ -367,8 +367,8 @@ def gated_fp4(x, gate, up):
                                         (40, 28672)])
 def test_gemv_fp4(n_tok, d_out, d_in):
     """One and several passes over the tokens, one and several tiles a CTA, rows
-    that end inside a unit, one panel and several, K in one part and in two (5201,
-    and 40 for 70 tokens).  (The smaller ones run on either kernel.)"""
+    that end inside a unit, one panel and several, K in one part and in two
+    (5201).  (The smaller ones run on either kernel.)"""
     assert fp4(n_tok, d_out, d_in) or d_out * d_in < 2 ** 24
     assert not fp4(1, 40, d_in)
     w = weights((d_out, d_in), d_out + d_in)
@@ -603,3 +603,39 @@ def test_swiglu_and_experts_of_few_columns_and_long_rows():
     B.nvfp4_gemv_experts(x, offsets, *w, z)
     by_expert(lambda r, *m: close(z[r], *sums_fp4(x[r], *m)), offsets, w)
     assert (z[0] == 7).all() and (z[7:] == 7).all()
+
+
+def test_fp4_halves_of_k_with_nonfinite_tokens():
+    d_out, d_in, n = 5201, 12544, 11
+    assert fp4(n, d_out, d_in)
+    w, x = weights((d_out, d_in), 7), acts(n, d_in, BF16, 8)
+    x[3, 9000], x[4, 5], x[10, 12543] = float("nan"), float("inf"), float("-inf")
+    y = torch.empty((n, d_out), device=DEV)
+    B.nvfp4_gemv(x, *w, y)
+    bad = [3, 4, 10]
+    keep = [t for t in range(n) if t not in bad]
+    close(y[keep], *sums_fp4(x[keep], w))
+    ref = (x[bad].double()[:, None, :] * dequantised(*w)[None]).sum(-1)
+    assert torch.equal(torch.isnan(y[bad]), torch.isnan(ref))
+    inf = torch.isinf(ref)
+    assert inf.any() and torch.equal(y[bad][inf].double(), ref[inf])
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 3, 17, 0, 2, 1, 9], [40, 17, 33, 0, 64, 2, 1, 16]])
+@pytest.mark.parametrize("pair,d_out", [(True, 1000), (False, 1004)])
+def test_fp4_halves_of_k_by_expert(counts, pair, d_out):
+    """One tile a pair of CTAs, and several pieces of several tiles."""
+    E, n, d_in = len(counts), sum(counts), 8192 if pair else 16384
+    assert fp4(n, d_out, d_in, E, pair)
+    ws_ = [weights((E, d_out, d_in), s) for s in ((15, 16) if pair else (15,))]
+    x = acts(n, d_in, BF16, 19) * 0.1
+    offsets = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device=DEV)
+    y = torch.empty((n, d_out), device=DEV)
+    ws = B.workspace(B.nvfp4_gemv_workspace_size(n, d_out, d_in, E, pair), DEV)
+    if pair:
+        B.nvfp4_gemv_swiglu_experts(x, offsets, *ws_, y, None, ws)
+    else:
+        B.nvfp4_gemv_experts(x, offsets, *ws_[0], y, None, ws)
+    assert B.nvfp4_workspace_status(ws) == 0
+    fn = gated_fp4 if pair else sums_fp4
+    by_expert(lambda r, *m: close(y[r], *fn(x[r], *m)), offsets, *ws_)
