@@ -447,15 +447,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
   auto step = [&] {
     if (++s == S) s = 0, ph ^= 1;
   };
-  // a copying role ends early: lets its copies issued so far land before the CTA exits
-  auto drain_copies = [&](uint64_t* bars, int issued) {
-    give_up(sh, a.status);
-    for (int k = 0; k < S && k < issued; ++k) {
-      if (--s < 0) s = S - 1, ph ^= 1;
-      mbar_wait_drain(&bars[s], ph);
-    }
-  };
-
+  int issued = 0;     // stages that a copying role has issued
   // The sums of tile no. g at output columns row ..: thread = column (TMEM lane),
   // tokens first, first + apart, ...  Warp-wide.  Each lane keeps the exponent of one
   // of the pass' tokens (32 at most): fetched when its token's turn comes, they took
@@ -520,7 +512,6 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
 
   if (warp == kCodeWarp) {
     // ---------------------------------------------------------------- codes and their scales
-    int issued = 0;
     bool ok = true;
     while (ok && pieces.next(a, &q)) {
       for (int64_t row = q.row0; ok && row < q.row1; row += a.tile) {
@@ -557,11 +548,10 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         }
       }
     }
-    if (!ok) drain_copies(sh->weights, issued);
+    if (!ok) give_up(sh, a.status);
   } else if (warp == kDigitWarp) {
     // ---------------------------------------------------------------- digits
     pdl_wait();
-    int issued = 0;
     bool ok = true;
     while (ok && pieces.next(a, &q)) {
       const uint32_t bytes = (uint32_t)(q.n * (1024 + 16) * P);
@@ -589,7 +579,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         }
       }
     }
-    if (!ok) drain_copies(sh->tokens, issued);
+    if (!ok) give_up(sh, a.status);
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- matrix instructions
     int g = 0, sf = 0;   // accumulators so far, buffer of scales
@@ -729,6 +719,24 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     if (!ok) give_up(sh, a.status);
   }
   __syncthreads();
+  // Some role gave up, maybe one that the copying roles never waited for (a CTA of no
+  // more stages than the ring has slots finds them all free): the copies that nobody
+  // has waited for land before the CTA exits.
+  if (aborted(sh) && (warp == kCodeWarp || warp == kDigitWarp)) {
+    uint64_t* bars = warp == kCodeWarp ? sh->weights : sh->tokens;
+    for (int k = 0; k < S && k < issued; ++k) {
+      if (--s < 0) s = S - 1, ph ^= 1;
+      mbar_wait_drain(&bars[s], ph);
+    }
+  }
+#ifdef NVFP4_DEBUG
+  // no copy is in flight, whichever way the roles ended (the first use of a slot has
+  // phase 0, its i-th i & 1)
+  if (warp == kCodeWarp || warp == kDigitWarp)
+    for (int k = max(issued - S, 0); k < issued; ++k)
+      if (!mbar_test_wait(warp == kCodeWarp ? &sh->weights[k % S] : &sh->tokens[k % S], k / S & 1))
+        atomicExch(a.status, (int)NVFP4_ERR_BOUNDS);
+#endif
   if (kSplit > 1) cluster_sync();   // (no CTA ends while the other may still write to it)
   if (warp == kMmaWarp) {
     tc_fence_after();
