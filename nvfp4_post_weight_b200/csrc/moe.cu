@@ -464,13 +464,17 @@ nvfp4_status nvfp4_moe_sort(const void* expert_ids, int id_bytes, int64_t n_tok,
   const int E = (int)n_experts, wide = id_bytes == 8, k = (int)top_k;
   const size_t smem = sizeof(int) * (kSortWarps + 1) * (size_t)E;
   const dim3 block(kSortWarps * 32);
-  static_assert(sizeof(int) * (kSortWarps + 1) * NVFP4_MAX_EXPERTS <= 227 * 1024, "shared memory");
-  if (smem > 48 * 1024) {
-    // (per device and kernel; setting it again is harmless)
+  // The limit is state of the kernel on this device that every thread's calls share, so
+  // it is always the largest call's, whatever this one needs: a call's own size could
+  // undercut another thread's between its setting and its launch.  (Static shared
+  // memory counts towards the 48 KB that need no setting: 372 experts are above it.)
+  constexpr int kMostSmem = sizeof(int) * (kSortWarps + 1) * NVFP4_MAX_EXPERTS;
+  static_assert(kMostSmem + 1024 <= 227 * 1024, "shared memory");
+  if (smem > 32 * 1024) {
     NVFP4_CUDA_TRY(cudaFuncSetAttribute(sort_small_kernel,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem));
     NVFP4_CUDA_TRY(cudaFuncSetAttribute(sort_place_kernel,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem));
   }
   if (n <= kSortOneCta || E == 0) {
     sort_small_kernel<<<1, block, smem, st>>>(expert_ids, wide, n, E, k, offsets, rows, position);

@@ -1,0 +1,69 @@
+"""Shared-memory limits of the routing and product kernels: sizes at the edge of
+what needs no setting, and calls of different sizes from several threads at once
+(the limit is state of a kernel that they share)."""
+import subprocess
+import sys
+import threading
+import os
+
+import pytest
+import torch
+
+from nvfp4_post_weight_b200 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+SORT = """
+import sys, torch
+from nvfp4_post_weight_b200 import binding as B
+E, T, k = int(sys.argv[1]), int(sys.argv[2]), 2
+i32 = dict(dtype=torch.int32, device="cuda:0")
+ids = torch.arange(T * k, **i32).view(T, k) % E
+off, rows, pos = torch.empty(E + 1, **i32), torch.empty(T * k, **i32), torch.empty((T, k), **i32)
+B.nvfp4_moe_sort(ids, off, rows, pos)
+order = torch.argsort(ids.flatten(), stable=True)
+assert torch.equal(rows.long(), order // k) and off[-1] == T * k
+"""
+
+
+@pytest.mark.parametrize("E", [248, 249, 371, 372, 373])
+@pytest.mark.parametrize("T", [400, 4000])
+def test_sort_of_experts_at_the_edge_of_the_default_limit(E, T):
+    """33 ints an expert and the static shared memory beside them: the first sort
+    of a process, before any larger one has raised the limit."""
+    subprocess.run([sys.executable, "-c", SORT, str(E), str(T)], check=True, cwd=ROOT, timeout=300)
+
+
+def together(*calls, times=3000):
+    """Runs the calls over and over in a thread each; the statuses but NVFP4_OK."""
+    bad = []
+
+    def loop(call):
+        for _ in range(times):
+            status = call()
+            if status:
+                bad.append(status)
+
+    threads = [threading.Thread(target=loop, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return bad
+
+
+def test_sorts_of_several_threads():
+    L = B.lib()
+    ids = torch.zeros((64, 2), dtype=torch.int32, device=DEV)
+
+    def sorts(E):
+        off, rows, pos = (torch.empty(n, dtype=torch.int32, device=DEV) for n in (E + 1, 128, 128))
+        ptrs = [t.data_ptr() for t in (off, rows, pos)]
+        st = torch.cuda.Stream()
+        keep = (off, rows, pos, st)
+        return lambda: keep and L.nvfp4_moe_sort(ids.data_ptr(), 4, 64, 2, E, *ptrs, st.cuda_stream)
+
+    assert together(*[sorts(E) for E in (1024, 400, 800, 380)]) == []
