@@ -329,12 +329,35 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
   }
 }
 
+// Chunks of tokens that are staged at a time, and the shared memory of a launch: the
+// staged planes of tok tokens and the sums of n_w matrices.
+constexpr int64_t stage_chunks(int planes, int64_t tok) {
+  const int64_t stage = kXSmem / (planes * tok * 256) / 4 * 4;
+  return stage < 4 ? 4 : stage;
+}
+constexpr int64_t smem_bytes(int planes, int n_w, int64_t tok, int64_t stage) {
+  return stage * planes * tok * 256 + (int64_t)sizeof(float) * n_w * tok * kRowsCta;
+}
+// The most that any call of one instantiation takes.
+constexpr int most_smem(int planes, int n_w, int nt) {
+  int64_t most = 0;
+  for (int64_t tok = 1; tok <= 8 * nt; ++tok) {
+    const int64_t bytes = smem_bytes(planes, n_w, tok, stage_chunks(planes, tok));
+    if (bytes > most) most = bytes;
+  }
+  return (int)most;
+}
+
 template <typename TX, int NW, int NT, bool kWide>
 nvfp4_status launch_kernel(const Args& a, dim3 grid, int S, size_t smem, cudaStream_t st) {
   auto kernel = product_kernel<TX, NW, NT, kWide>;
+  // (always the largest call's: the limit is state of the kernel on this device that
+  // other threads' calls of other sizes share)
+  constexpr int kMostSmem = most_smem(sizeof(TX) == 2 ? 1 : 3, NW, NT);
+  static_assert(kMostSmem <= 226 * 1024, "shared memory");
   if (smem > 48 * 1024)
     NVFP4_CUDA_TRY(
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem));
   if (S > 8)
     NVFP4_CUDA_TRY(
         cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
@@ -400,12 +423,10 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
   a.slice = (n_chunks + S - 1) / S;
   const int64_t tok = p.n_rows < 8 * nt ? p.n_rows : 8 * nt;
   const int planes = p.x_bf16 ? 1 : 3;
-  const int64_t per_chunk = planes * tok * 256;
-  int64_t stage = kXSmem / per_chunk / 4 * 4;
-  if (stage < 4) stage = 4;
+  int64_t stage = stage_chunks(planes, tok);
   if (stage > a.slice) stage = (a.slice + 3) / 4 * 4;
   a.stage = (int)stage;
-  const size_t smem = stage * per_chunk + sizeof(float) * p.n_w * tok * kRowsCta;
+  const size_t smem = smem_bytes(planes, p.n_w, tok, stage);
   bool wide = p.d_in % 32 == 0;
   for (int m = 0; m < p.n_w; ++m)
     wide = wide && (reinterpret_cast<uintptr_t>(p.codes[m]) & 15) == 0 &&

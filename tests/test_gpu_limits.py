@@ -67,3 +67,26 @@ def test_sorts_of_several_threads():
         return lambda: keep and L.nvfp4_moe_sort(ids.data_ptr(), 4, 64, 2, E, *ptrs, st.cuda_stream)
 
     assert together(*[sorts(E) for E in (1024, 400, 800, 380)]) == []
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_products_of_several_threads(dtype):
+    """Sizes that one kernel serves with 60 to 80 KB of shared memory of bf16 tokens,
+    84 to 112 KB of fp32 ones."""
+    L = B.lib()
+    d_out, d_in = 16, 16384 if dtype == torch.bfloat16 else 512
+    codes = torch.randint(0, 256, (d_out, d_in // 2), dtype=torch.uint8, device=DEV)
+    scales = torch.full((d_out, d_in // 16), 56, dtype=torch.uint8, device=DEV)
+    sg = torch.ones(1, device=DEV)
+    w = [t.data_ptr() for t in (codes, scales, sg)]
+
+    def products(n):
+        assert B.nvfp4_gemv_workspace_size(n, d_out, d_in, dtype=dtype) == 0
+        x, y = torch.ones((n, d_in), dtype=dtype, device=DEV), torch.empty((n, d_out), device=DEV)
+        st = torch.cuda.Stream()
+        keep = (x, y, st, codes, scales, sg)
+        t = 0 if dtype == torch.bfloat16 else 1
+        return lambda: keep and L.nvfp4_gemv(x.data_ptr(), t, n, *w, d_out, d_in, y.data_ptr(), 1,
+                                             None, 0, st.cuda_stream)
+
+    assert together(*[products(n) for n in (32, 24, 30, 25)], times=10000) == []
