@@ -594,7 +594,7 @@ nvfp4_status nvfp4_gemv_experts(const void* X, nvfp4_dtype x_dtype, int64_t n_x,
                                 nvfp4_dtype y_dtype, void* ws, size_t ws_bytes,
                                 nvfp4_stream_t stream) {
   if (n_experts > 0 && n_rows > 0 && !offsets) return NVFP4_ERR_INVALID_ARG;
-  if (!rows && n_x != n_rows) return NVFP4_ERR_INVALID_ARG;
+  if (!rows && n_rows > 0 && n_x != n_rows) return NVFP4_ERR_INVALID_ARG;
   const Matrix w[1] = {{codes, scales, global_scales}};
   return product(X, x_dtype, n_x, rows, offsets, n_experts, n_rows, w, 1, d_out, d_in, Y, y_dtype,
                  ws, ws_bytes, stream);
@@ -607,7 +607,7 @@ nvfp4_status nvfp4_gemv_swiglu_experts(
     const float* up_global_scales, int64_t d_out, int64_t d_in, void* Y, nvfp4_dtype y_dtype,
     void* ws, size_t ws_bytes, nvfp4_stream_t stream) {
   if (n_experts > 0 && n_rows > 0 && !offsets) return NVFP4_ERR_INVALID_ARG;
-  if (!rows && n_x != n_rows) return NVFP4_ERR_INVALID_ARG;
+  if (!rows && n_rows > 0 && n_x != n_rows) return NVFP4_ERR_INVALID_ARG;
   const Matrix w[2] = {{gate_codes, gate_scales, gate_global_scales},
                        {up_codes, up_scales, up_global_scales}};
   return product(X, x_dtype, n_x, rows, offsets, n_experts, n_rows, w, 2, d_out, d_in, Y, y_dtype,

@@ -218,3 +218,11 @@ def test_a_stream_or_tensor_of_another_device_is_refused(monkeypatch):
     monkeypatch.setattr(B, "lib", L)
     B._run_on("nvfp4_gemv", 0, stream, 5)
     assert seen == [0, (5, 7), "out"]
+
+
+def test_no_sorted_rows_need_no_row_indices():
+    """An empty array has no address: rows of no entries are as good as any."""
+    for f, w in ((B.lib().nvfp4_gemv_experts, (A, A, A)),
+                 (B.lib().nvfp4_gemv_swiglu_experts, (A,) * 6)):
+        assert f(A, 0, 3, None, A, 2, 0, *w, 16, 32, None, 0, None, 0, None) == OK
+        assert f(A, 0, 3, None, A, 2, 1, *w, 16, 32, A, 0, None, 0, None) == ARG
