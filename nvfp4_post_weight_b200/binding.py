@@ -704,7 +704,7 @@ def _run_on(call, dev, stream, *args):
 def _weight(call, name, w, lead, d_out, d_in, dev):
     """Pointers of (codes, scales, global_scale) of one matrix (lead = ()) or of
     lead[0] experts' matrices one after another."""
-    if len(w) != 3:
+    if not isinstance(w, (tuple, list)) or len(w) != 3:
         raise Nvfp4Error(call, NVFP4_ERR_INVALID_ARG, f"{name}: expected (codes, scales, "
                                                       f"global_scale)")
     return (_arg(call, w[0], name + "codes", (*lead, d_out, d_in // 2), _U8, dev),

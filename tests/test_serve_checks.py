@@ -226,3 +226,10 @@ def test_no_sorted_rows_need_no_row_indices():
                  (B.lib().nvfp4_gemv_swiglu_experts, (A,) * 6)):
         assert f(A, 0, 3, None, A, 2, 0, *w, 16, 32, None, 0, None, 0, None) == OK
         assert f(A, 0, 3, None, A, 2, 1, *w, 16, 32, A, 0, None, 0, None) == ARG
+
+
+@pytest.mark.parametrize("w", [None, 5, torch.zeros((3, 4)), (None, None)])
+def test_a_weight_is_three_tensors(w):
+    with pytest.raises(B.Nvfp4Error, match="expected \\(codes, scales, global_scale\\)") as e:
+        B._weight("nvfp4_gemv_swiglu", "gate ", w, (), 16, 32, 0)
+    assert e.value.code == ARG
