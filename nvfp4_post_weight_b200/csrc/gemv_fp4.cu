@@ -4,15 +4,19 @@
 // tokens are taken apart into FP4 digits instead.
 //
 // Digits: a 16-element block of a token is a fixed-point integer
-// v = rn(x 2^(21 - eb)), |v| <= 2^22, eb the exponent of the block's largest
-// entry, written with eight digits -4 .. 3 of base 8, all of them E2M1 values;
-// the block's power of two 2^(eb - E) (E: the token's largest exponent) is its
-// E4M3 scale.  Each token is eight columns of the product, and
-// x . q = 2^(E - 29) sum_p 8^p D_p.  The products are exact; a column is summed
-// in fp32 by the matrix unit.  An entry is kept to 2^-22 of the largest of its
-// block, or to 2^-39 of the token's largest (blocks more than 17 octaves below
-// it), and bf16 entries within 2^-14 of their block's largest are exact.  (fp32
-// tokens would lose bits of every entry; they take the other kernel.)
+// v = rn(x 2^(27 - eb)), |v| <= 2^28, eb the exponent of the block's largest
+// entry, written with eight digits of base 13, each one of 0, +-1, +-2, +-3, +-4,
+// +-6, +-8: one of them for every remainder, and half of each an E2M1 value.  The
+// block's power of two 2^(eb - E) (E: the token's largest exponent) is its E4M3
+// scale.  Each token is eight columns of the product, and
+// x . q = 2^(E - 34) sum_p 13^p D_p.  The products are exact; a column is summed
+// in fp32 by the matrix unit.  An entry is kept to 2^-28 of the largest of its
+// block, or to 2^-45 of the token's largest (blocks more than 17 octaves below
+// it), and bf16 entries within 2^-20 of their block's largest are exact: an output
+// whose weight at a block's outlier is zero keeps the others' bits.  (Digits -4 .. 3
+// of base 8, 22 bits: one entry of 10^4 among 8191 of N(0, 1) left 4e-5 of relative
+// error there.  fp32 tokens would lose bits of every entry; they take the other
+// kernel.)
 //
 // Nothing is decoded: one warp has the weights copied, one the digits, one issues
 // the matrix instructions (an N <= 64 takes 45 cycles, N = 128 64), three groups
@@ -112,6 +116,16 @@ __device__ __forceinline__ int64_t x_row(const Product& p, int64_t r) {
   return x < p.n_x ? x : -1;
 }
 
+// Half a digit as E2M1 code by the remainder that it leaves: 0, 1, 2, 3, 4, -8, 6, -6,
+// 8, -4, -3, -2, -1.
+constexpr uint64_t kDigitCodes = 0x9ABC6D5E43210ull;
+// The eighth digit is what seven leave of |v| <= 2^28: at most 2^28 / 13^7 + 8 / 12 < 5.
+// Five are added for it at the start: codes of -4 .. 4 for 1 .. 9.
+constexpr int kBias = 5 * 62748517;   // 5 * 13^7
+constexpr uint64_t kTopCodes = 0x432109ABC0ull;
+// u / 13 for u < 2^30: 13 * 330382100 = 2^32 + 4.
+__device__ __forceinline__ uint32_t div13(uint32_t u) { return __umulhi(u, 330382100u); }
+
 __global__ void __launch_bounds__(kDigitThreads)
     digits_kernel(const Product p, uint8_t* __restrict__ digits,
                   uint8_t* __restrict__ sf, int* __restrict__ expo, int* status) {
@@ -149,26 +163,30 @@ __global__ void __launch_bounds__(kDigitThreads)
   for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));   // a block is two lanes' entries
   const int below = min(E - exponent(most), 17);
-  const int up = 21 - (E - below);                 // 2^up in two factors of fp32's range
+  const int up = 27 - (E - below);                 // 2^up in two factors of fp32's range
   const float s0 = __uint_as_float((uint32_t)(up / 2 + 127) << 23);
   const float s1 = __uint_as_float((uint32_t)(up - up / 2 + 127) << 23);
-  uint32_t u[8];
+  uint32_t u[8];   // what is left of each entry, made positive for the first seven digits
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    // rounded to an integer by the addition (|v| <= 2^22), then made a sum of
-    // digits 0 .. 7 by adding 4 at every place
-    const float v = __fadd_rn(f[j] * s0 * s1, 0x1.8p23f);
-    u[j] = __float_as_uint(v) - 0x4B400000u + 9586980u;
-  }
+  for (int j = 0; j < 8; ++j) u[j] = (uint32_t)(__float2int_rn(f[j] * s0 * s1) + kBias);
   const int panel = k / kPanelK, byte = (k % kPanelK) / 2;
   const int64_t at = panel * p.n_rows + r;
   uint8_t* out = digits + at * 1024;
 #pragma unroll
   for (int p = 0; p < 8; ++p) {
-    uint32_t word = 0;   // E2M1 codes of -4 .. 3, first element lowest
+    uint32_t word = 0;   // E2M1 codes, first element lowest
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      word |= ((0x5420ACDEu >> (4 * (u[j] >> (3 * p) & 7u))) & 0xFu) << (4 * j);
+    for (int j = 0; j < 8; ++j) {
+      uint32_t code;
+      if (p < 7) {
+        const uint32_t q = div13(u[j]);
+        code = (uint32_t)(kDigitCodes >> 4 * (u[j] - 13 * q)) & 0xFu;
+        u[j] = q + (code >> 3);   // a digit below zero borrowed 13
+      } else {
+        code = (uint32_t)(kTopCodes >> 4 * u[j]) & 0xFu;
+      }
+      word |= code << (4 * j);
+    }
     *reinterpret_cast<uint32_t*>(out + p * 128 + ((((byte >> 4) ^ p) & 7) << 4) + (byte & 15)) =
         word;
   }
@@ -479,9 +497,15 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
       for (int k = 0; k < 2; ++k) {
         const int w = k * (NW - 1), i = NW == 2 || k == 0 ? i0 : second;
         const int E = __shfl_sync(~0u, exponent, i);
-        float sum = c[k][7];
+        // sum_p 13^p D_p, four digits exactly for a single product before the one rounding
+        // that joins them
+        float high = c[k][7], low = c[k][3];
 #pragma unroll
-        for (int p = 6; p >= 0; --p) sum = fmaf(sum, 8.f, c[k][p]);
+        for (int p = 2; p >= 0; --p) {
+          high = fmaf(high, 13.f, c[k][p + 4]);
+          low = fmaf(low, 13.f, c[k][p]);
+        }
+        float sum = fmaf(high, 28561.f, low);
         const int at = (i * NW + w) * kTile + (threadIdx.x & (kTile - 1));
         if (rank > 0) {
           cluster_store(to + 4 * at, sum);
@@ -489,7 +513,7 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
         }
         if (kSplit > 1) sum += part[at];
         if (o < o_end) {
-          const double scale = __hiloint2double((E - 29 + 1023) << 20, 0);
+          const double scale = __hiloint2double((E - 34 + 1023) << 20, 0);
           v[k] = E == kNonFinite ? plain_product(a.p, w, q.e, x_row(a.p, q.t0 + i), o)
                                  : (float)((double)sum * (scale * (double)sg[w]));
         }
