@@ -13,10 +13,15 @@
 // in fp32 by the matrix unit.  An entry is kept to 2^-28 of the largest of its
 // block, or to 2^-45 of the token's largest (blocks more than 17 octaves below
 // it), and bf16 entries within 2^-20 of their block's largest are exact: an output
-// whose weight at a block's outlier is zero keeps the others' bits.  (Digits -4 .. 3
-// of base 8, 22 bits: one entry of 10^4 among 8191 of N(0, 1) left 4e-5 of relative
-// error there.  fp32 tokens would lose bits of every entry; they take the other
-// kernel.)
+// whose weight at a block's outlier is zero keeps the others' bits.  What is left out
+// of a block is added by the warps that write the outputs where it may be more than
+// 2^-20 of the token's typical magnitude: of 2^m, m the mean exponent of the largest of
+// every eight entries, all zeros aside.  (That takes an outlier some 2^9 above the
+// others which has entries 2^-20 of itself in its block: one in ten of 8191 tokens of
+// N(0, 1) beside 2^13, all beside 2^20.)  Digits -4 .. 3 of base 8, 22 bits, left 4e-5
+// of relative error beside one entry of 10^4 among 8191 of N(0, 1), 3e-3 beside 10^6,
+// where now 9e-8 and 2e-7 are left.  fp32 tokens would lose bits of every entry; they
+// take the other kernel.
 //
 // Nothing is decoded: one warp has the weights copied, one the digits, one issues
 // the matrix instructions (an N <= 64 takes 45 cycles, N = 128 64), three groups
@@ -26,10 +31,10 @@
 // do not mix), 256 or 512 columns of K a stage.  Where few rows have many columns, two
 // CTAs share the columns: the second's sums go to the first's shared memory.
 //
-// What bounds it: one token's DRAM bytes (the 28672 x 8192 pair, 264 MB in 49.6
-// us, 82% of the copy rate); with more tokens the traffic from L2 to the SMs, where
+// What bounds it: one token's DRAM bytes (the 28672 x 8192 pair, 264 MB in 51 us, 80%
+// of the copy rate); with more tokens the traffic from L2 to the SMs, where
 // every CTA reads all digits, four bytes an entry, beside its rows (the pair with
-// 32 tokens, two passes, 0.84 GB in 94 us); with few rows an SM the chain of
+// 32 tokens, two passes, 0.84 GB in 97 us); with few rows an SM the chain of
 // stages (some 0.25 us per 256 columns).  Loading scales through registers instead
 // of TMA took 58 us for the one-token pair, copies of scales by tcgen05.cp from
 // the issuing thread 95 us, a single warp lane's non-uniform loop 68 us.
@@ -69,6 +74,7 @@ constexpr int kUnit = 8;                          // output columns that are sha
 constexpr int kSmem = 225 * 1024;
 constexpr int kTmemCols = 512;                    // sums, then buffers of a stage's scales
 constexpr int kNonFinite = 0x7FFFFFFF;            // in place of a token's exponent
+constexpr int kLeftOut = 1 << 20;                 // added to one that has blocks to complete
 
 struct Fp4Args {
   // codes and scales of each matrix in boxes of tile and of 32 rows by one stage
@@ -77,6 +83,7 @@ struct Fp4Args {
   const uint8_t* digits;    // per panel and sorted row: 8 x 128 bytes, 128-byte swizzle
   const uint8_t* sf;        // per panel and sorted row: 16 scale codes
   const int* expo;          // per sorted row: E or kNonFinite
+  const uint16_t* blocks;   // per sorted row and panel: a bit per block to be completed
   int* status;
   int panels;               // per stage
   int n_stages;             // of K
@@ -126,74 +133,117 @@ constexpr uint64_t kTopCodes = 0x432109ABC0ull;
 // u / 13 for u < 2^30: 13 * 330382100 = 2^32 + 4.
 __device__ __forceinline__ uint32_t div13(uint32_t u) { return __umulhi(u, 330382100u); }
 
+// f 2^e, |e| <= 252, in two steps that stay in fp32's range.
+__device__ __forceinline__ float scaled(float f, int e) {
+  return f * __uint_as_float((uint32_t)(e / 2 + 127) << 23) *
+         __uint_as_float((uint32_t)(e - e / 2 + 127) << 23);
+}
+
+// Entries of a row of block masks: one per panel, and zeros up to whole 16-byte words.
+__host__ __device__ constexpr int mask_stride(int n_panels) { return (n_panels + 7) / 8 * 8; }
+
+// Magnitude bits of the largest of eight entries.
+__device__ __forceinline__ uint32_t largest(const float* f) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  return most;
+}
+
 __global__ void __launch_bounds__(kDigitThreads)
-    digits_kernel(const Product p, uint8_t* __restrict__ digits,
-                  uint8_t* __restrict__ sf, int* __restrict__ expo, int* status) {
+    digits_kernel(const Product p, uint8_t* __restrict__ digits, uint8_t* __restrict__ sf,
+                  int* __restrict__ expo, uint16_t* __restrict__ blocks, int* status) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  __shared__ uint32_t warp_max[kDigitThreads / 32];
+  constexpr int kWarps = kDigitThreads / 32;
+  __shared__ uint32_t warp_max[kWarps];
+  __shared__ int warp_sum[kWarps], warp_count[kWarps];
   const int64_t r = blockIdx.x;
   const int d_in = (int)p.d_in;
   const int64_t row = x_row(p, r);
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.X) + row * d_in;
   if (r == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
-  // the row's largest magnitude (bits order like values; not finite: above all)
+  // the row's largest magnitude (bits order like values; not finite: above all), and the
+  // exponents of the largest of every eight entries that are not all zero, summed, and
+  // their number
   uint32_t big = 0;
+  int sum = 0, count = 0;
   if (row >= 0)
 #pragma unroll 4
     for (int k = threadIdx.x * 8; k < d_in; k += kDigitThreads * 8) {
       float f[8];
       load8(x + k, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) big = max(big, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+      const uint32_t most = largest(f);
+      big = max(big, most);
+      if (most) sum += exponent(most), ++count;
     }
-  for (int d = 16; d > 0; d >>= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, d));
-  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = big;
+  big = __reduce_max_sync(0xffffffffu, big);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  count = __reduce_add_sync(0xffffffffu, count);
+  if ((threadIdx.x & 31) == 0) {
+    warp_max[threadIdx.x >> 5] = big;
+    warp_sum[threadIdx.x >> 5] = sum;
+    warp_count[threadIdx.x >> 5] = count;
+  }
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kDigitThreads / 32; ++w) big = max(big, warp_max[w]);
+  const int w = threadIdx.x & (kWarps - 1);   // (sums of all warps, twice: 32 lanes)
+  big = __reduce_max_sync(0xffffffffu, warp_max[w]);
+  sum = __reduce_add_sync(0xffffffffu, warp_sum[w]);
+  count = __reduce_add_sync(0xffffffffu, warp_count[w]);
   const bool finite = big < 0x7F800000u;
   const int E = exponent(big);
   if (blockIdx.y == 0 && threadIdx.x == 0) expo[r] = finite ? E : kNonFinite;
   const int k = blockIdx.y * kDigitCols + threadIdx.x * 8;
-  if (k >= d_in) return;
+  const bool in = k < d_in;   // (warp-uniform: whole panels)
   float f[8] = {};
-  if (row >= 0 && finite) load8(x + k, f);
-  uint32_t most = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  if (in && row >= 0 && finite) load8(x + k, f);
+  uint32_t most = largest(f);
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));   // a block is two lanes' entries
   const int below = min(E - exponent(most), 17);
-  const int up = 27 - (E - below);                 // 2^up in two factors of fp32's range
-  const float s0 = __uint_as_float((uint32_t)(up / 2 + 127) << 23);
-  const float s1 = __uint_as_float((uint32_t)(up - up / 2 + 127) << 23);
+  const int up = 27 - (E - below);
   uint32_t u[8];   // what is left of each entry, made positive for the first seven digits
+  bool whole = true;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) u[j] = (uint32_t)(__float2int_rn(f[j] * s0 * s1) + kBias);
-  const int panel = k / kPanelK, byte = (k % kPanelK) / 2;
-  const int64_t at = panel * p.n_rows + r;
-  uint8_t* out = digits + at * 1024;
-#pragma unroll
-  for (int p = 0; p < 8; ++p) {
-    uint32_t word = 0;   // E2M1 codes, first element lowest
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      uint32_t code;
-      if (p < 7) {
-        const uint32_t q = div13(u[j]);
-        code = (uint32_t)(kDigitCodes >> 4 * (u[j] - 13 * q)) & 0xFu;
-        u[j] = q + (code >> 3);   // a digit below zero borrowed 13
-      } else {
-        code = (uint32_t)(kTopCodes >> 4 * u[j]) & 0xFu;
-      }
-      word |= code << (4 * j);
-    }
-    *reinterpret_cast<uint32_t*>(out + p * 128 + ((((byte >> 4) ^ p) & 7) << 4) + (byte & 15)) =
-        word;
+  for (int j = 0; j < 8; ++j) {
+    const float at = scaled(f[j], up);
+    u[j] = (uint32_t)(__float2int_rn(at) + kBias);
+    // (eight bits from 2^7 on are whole; below, what an integer's addition rounds away)
+    const float rest = at - (__fadd_rn(at, 0x1.8p23f) - 0x1.8p23f);
+    whole = whole && (fabsf(at) >= 128.f || (rest == 0.f && (at != 0.f || f[j] == 0.f)));
   }
-  if ((threadIdx.x & 1) == 0) {
-    // 2^(8 - below) in E4M3: normal down to 2^-6, then 2^-7, 2^-8, 2^-9
-    const int code = below <= 14 ? (15 - below) << 3 : 4 >> (below - 15);
-    sf[at * 16 + (k % kPanelK) / 16] = (uint8_t)code;
+  // half a unit of v is 2^(E - below - 28): above 2^(sum / count - 20)?
+  const unsigned open = __ballot_sync(0xffffffffu, !whole && (E - below - 8) * count > sum);
+  if ((threadIdx.x & 31) == 0 && k / kPanelK < mask_stride(d_in / kPanelK)) {
+    uint32_t bits = 0;   // a block's two lanes to one bit
+    for (int b = 0; open && b < 16; ++b) bits |= (uint32_t)((open >> (2 * b) & 3u) != 0) << b;
+    blocks[r * mask_stride(d_in / kPanelK) + k / kPanelK] = (uint16_t)bits;
+  }
+  if (in) {
+    const int panel = k / kPanelK, byte = (k % kPanelK) / 2;
+    const int64_t at = panel * p.n_rows + r;
+    uint8_t* out = digits + at * 1024;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      uint32_t word = 0;   // E2M1 codes, first element lowest
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t code;
+        if (p < 7) {
+          const uint32_t q = div13(u[j]);
+          code = (uint32_t)(kDigitCodes >> 4 * (u[j] - 13 * q)) & 0xFu;
+          u[j] = q + (code >> 3);   // a digit below zero borrowed 13
+        } else {
+          code = (uint32_t)(kTopCodes >> 4 * u[j]) & 0xFu;
+        }
+        word |= code << (4 * j);
+      }
+      *reinterpret_cast<uint32_t*>(out + p * 128 + ((((byte >> 4) ^ p) & 7) << 4) + (byte & 15)) =
+          word;
+    }
+    if ((threadIdx.x & 1) == 0) {
+      // 2^(8 - below) in E4M3: normal down to 2^-6, then 2^-7, 2^-8, 2^-9
+      const int code = below <= 14 ? (15 - below) << 3 : 4 >> (below - 15);
+      sf[at * 16 + (k % kPanelK) / 16] = (uint8_t)code;
+    }
   }
 }
 
@@ -386,22 +436,46 @@ struct Pieces {
   }
 };
 
-// One product x . q by plain sums: row x of X, column o of matrix w of expert e.
-// For tokens that digits cannot stand for (a NaN or an infinity among them).
-__device__ __noinline__ float plain_product(const Product& p, int w, int e, int64_t x, int64_t o) {
+// One product x . q where digits do not do, sorted row r, column o of matrix w of expert
+// e.  A token with a NaN or an infinity: by plain sums.  One with blocks to complete:
+// the digits' product and what they leave out of those.  Warp-wide, each lane its own
+// column: the lanes have an entry of the block each and hand it round.  (Some 3.5 us for
+// a token with one block: round trips to memory one after another.  A call of its own, so
+// that the loops that have no such token keep their registers.)
+__device__ __noinline__ float special_product(const Fp4Args& a, int w, int e, int64_t r, int64_t o,
+                                              int E, double digits) {
+  const Product& p = a.p;
+  const int lane = threadIdx.x & 31, n_panels = p.nb / 16;
   const int64_t block = (e * p.d_out + o) * p.nb;
   const uint2* codes = reinterpret_cast<const uint2*>(p.codes[w]) + block;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.X) + x_row(p, r) * p.d_in;
+  const uint16_t* masks = a.blocks + r * mask_stride(n_panels);
+  const bool plain = E == kNonFinite - kLeftOut;
   float sum = 0.f;
-  for (int b = 0; b < p.nb; ++b) {
-    const uint2 c = codes[b];
-    const float scale = (float)e4m3_value(p.scales[w][block + b] & 0x7F);
-    for (int j = 0; j < kBlock; ++j) {
-      const int64_t k = x * p.d_in + b * kBlock + j;
-      const float v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.X)[k]);
-      sum = fmaf(v, e2m1_value((j < 8 ? c.x : c.y) >> (4 * (j & 7)) & 0xF) * scale, sum);
+  for (int first = 0; first < n_panels; first += 32) {
+    uint32_t mine = 0;   // the blocks of panel first + lane
+    if (first + lane < n_panels) mine = plain ? 0xFFFFu : masks[first + lane];
+    for (unsigned some = __ballot_sync(~0u, mine != 0); some; some &= some - 1) {
+      const int at = __ffs(some) - 1;
+      for (uint32_t bits = __shfl_sync(~0u, mine, at); bits; bits &= bits - 1) {
+        const int b = (first + at) * 16 + __ffs(bits) - 1;
+        const uint2 c = codes[b];
+        const float scale = (float)e4m3_value(p.scales[w][block + b] & 0x7F);
+        float f = lane < kBlock ? __bfloat162float(x[b * kBlock + lane]) : 0.f;
+        if (!plain) {
+          const uint32_t most = __reduce_max_sync(~0u, __float_as_uint(f) & 0x7FFFFFFFu);
+          const int up = 27 - max(exponent(most), E - 17);
+          f -= scaled(rintf(scaled(f, up)), -up);
+        }
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j)
+          sum = fmaf(__shfl_sync(~0u, f, j),
+                     e2m1_value((j < 8 ? c.x : c.y) >> (4 * (j & 7)) & 0xF) * scale, sum);
+      }
     }
   }
-  return sum * p.sg[w][e];
+  const double sg = p.sg[w][e];
+  return plain ? sum * (float)sg : (float)(digits + (double)sum * sg);
 }
 
 template <int NW, int kSplit>
@@ -472,9 +546,23 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
   // the down projections of 64 tokens 18 us longer.  Two sums a round trip to tensor
   // memory instead of one: 88 to 84 us.
   int exponent = 0;
+  bool any_special = false;
   float sg[NW];
   auto enter_pass = [&](const Piece& q) {
-    exponent = lane < q.n ? __ldg(a.expo + q.t0 + lane) : 0;
+    exponent = 0;
+    if (lane < q.n) {
+      exponent = __ldg(a.expo + q.t0 + lane);
+      const int words = mask_stride(a.p.nb / 16) / 8;
+      const uint4* masks = reinterpret_cast<const uint4*>(a.blocks) + (int64_t)(q.t0 + lane) * words;
+      uint32_t left = 0;
+#pragma unroll 4
+      for (int i = 0; i < words; ++i) {
+        const uint4 m = __ldg(masks + i);
+        left |= m.x | m.y | m.z | m.w;
+      }
+      if (left) exponent += kLeftOut;
+    }
+    any_special = __any_sync(~0u, exponent >= kLeftOut / 2);
 #pragma unroll
     for (int w = 0; w < NW; ++w) sg[w] = __ldg(a.p.sg[w] + q.e);
   };
@@ -485,8 +573,23 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
     if (rank == 0 && kSplit > 1 && !wait_cluster(&sh->part_full, g & 1, limit, sh)) return false;
     tc_fence_after();
     const uint32_t to = rank > 0 ? cluster_addr(part, 0) : 0;
-    const int64_t o = row + (threadIdx.x & (kTile - 1)), o_end = min(row + a.tile, q.row1);
+    const int col = threadIdx.x & (kTile - 1);
+    const int64_t o = row + col, o_end = min(row + a.tile, q.row1);
     const uint32_t d = tmem + ((uint32_t)((warp & 3) * 32) << 16) + buf * NW * columns;
+    // sum_p 13^p D_p, four digits exactly for a single product before the one rounding
+    // that joins them
+    auto join = [&](const float* c) {
+      float high = c[7], low = c[3];
+#pragma unroll
+      for (int p = 2; p >= 0; --p) {
+        high = fmaf(high, 13.f, c[p + 4]);
+        low = fmaf(low, 13.f, c[p]);
+      }
+      return fmaf(high, 28561.f, low);
+    };
+    auto value = [&](float sum, int E, int w) {
+      return (double)sum * (__hiloint2double((E - 34 + 1023) << 20, 0) * (double)sg[w]);
+    };
     // two sums at a time: both matrices' of a token, or one matrix' of two tokens
     constexpr int kTokens = 2 / NW;
     for (int i0 = first; i0 < q.n; i0 += apart * kTokens) {
@@ -497,32 +600,38 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
       for (int k = 0; k < 2; ++k) {
         const int w = k * (NW - 1), i = NW == 2 || k == 0 ? i0 : second;
         const int E = __shfl_sync(~0u, exponent, i);
-        // sum_p 13^p D_p, four digits exactly for a single product before the one rounding
-        // that joins them
-        float high = c[k][7], low = c[k][3];
-#pragma unroll
-        for (int p = 2; p >= 0; --p) {
-          high = fmaf(high, 13.f, c[k][p + 4]);
-          low = fmaf(low, 13.f, c[k][p]);
-        }
-        float sum = fmaf(high, 28561.f, low);
-        const int at = (i * NW + w) * kTile + (threadIdx.x & (kTile - 1));
+        float sum = join(c[k]);
+        const int at = (i * NW + w) * kTile + col;
         if (rank > 0) {
           cluster_store(to + 4 * at, sum);
           continue;
         }
         if (kSplit > 1) sum += part[at];
-        if (o < o_end) {
-          const double scale = __hiloint2double((E - 34 + 1023) << 20, 0);
-          v[k] = E == kNonFinite ? plain_product(a.p, w, q.e, x_row(a.p, q.t0 + i), o)
-                                 : (float)((double)sum * (scale * (double)sg[w]));
-        }
+        if (o < o_end) v[k] = (float)value(sum, E, w);
       }
       if (rank == 0 && o < o_end) {
         write_product<NW>(a.p, v, q.t0 + i0, o);
         if (NW == 1 && i0 + apart < q.n) write_product<NW>(a.p, v + 1, q.t0 + second, o);
       }
     }
+    // once more for tokens that digits alone do not stand for (kept apart: with the call in
+    // the loop above its registers spill)
+    if (rank == 0 && any_special)
+      for (int i = first; i < q.n; i += apart) {
+        const int E = __shfl_sync(~0u, exponent, i);
+        if (E < kLeftOut / 2) continue;
+        float c[2][8], v[2];
+        tmem_ld8_twice(d + 8 * i, d + (NW - 1) * columns + 8 * i, c);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          float sum = join(c[w]);
+          if (kSplit > 1) sum += part[(i * NW + w) * kTile + col];
+          v[w] = special_product(a, w, q.e, q.t0 + i, min(o, o_end - 1), E - kLeftOut,
+                                 value(sum, E - kLeftOut, w));
+        }
+        if (o < o_end) write_product<NW>(a.p, v, q.t0 + i, o);
+        __syncwarp();
+      }
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
@@ -778,7 +887,8 @@ bool product_fp4_shape(int64_t n_rows, int64_t d_in) {
 
 size_t product_fp4_ws_bytes(int64_t n_rows, int64_t d_in) {
   const size_t rows = n_rows, n = panels_of(d_in);
-  return kWsHeader + align256(rows * sizeof(int)) + align256(rows * n * 16) + rows * n * 1024;
+  return kWsHeader + align256(rows * sizeof(int)) + align256(rows * mask_stride(n) * 2) +
+         align256(rows * n * 16) + rows * n * 1024;
 }
 
 bool product_fp4_supported(const Product& p) {
@@ -800,14 +910,17 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
   w += kWsHeader;
   int* expo = reinterpret_cast<int*>(w);
   w += align256(rows * sizeof(int));
+  uint16_t* blocks = reinterpret_cast<uint16_t*>(w);
+  w += align256(rows * mask_stride(n_panels) * 2);
   uint8_t* sf = reinterpret_cast<uint8_t*>(w);
   w += align256(rows * n_panels * 16);
   uint8_t* digits = reinterpret_cast<uint8_t*>(w);
   a.expo = expo;
+  a.blocks = blocks;
   a.sf = sf;
   a.digits = digits;
   const dim3 grid((unsigned)p.n_rows, (unsigned)((p.d_in + kDigitCols - 1) / kDigitCols));
-  digits_kernel<<<grid, kDigitThreads, 0, st>>>(p, digits, sf, expo, a.status);
+  digits_kernel<<<grid, kDigitThreads, 0, st>>>(p, digits, sf, expo, blocks, a.status);
   NVFP4_LAUNCH_CHECK();
   // tokens per pass: what the accumulators hold, in equal passes; for experts
   // 16, so that an expert's rows of a small batch take one pass
