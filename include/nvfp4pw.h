@@ -477,7 +477,8 @@ nvfp4_status nvfp4_dequant_batched(int count, const uint8_t* const* codes,
  *           0, x_dtype) bytes, 256-byte aligned (0 for calls that need none,
  *           NULL is then fine).  Its first int is the status word
  *           (nvfp4_workspace_status): a timed-out wait sets
- *           NVFP4_ERR_TIMEOUT, Y is then unspecified.
+ *           NVFP4_ERR_TIMEOUT, Y is then unspecified.  nvfp4_product_status
+ *           tells of it too, when the workspace is gone.
  * The products are exact, their sums fp32, and Y is rounded once.  Calls that
  * need a workspace run on the block-scaled FP4 tensor cores where codes and
  * scales are 16-byte aligned: there a (bf16) token's entry is kept to 2^-28 of
@@ -508,6 +509,13 @@ nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const
  * used, the largest answer serves them all.  0 for sizes that a call refuses. */
 size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts,
                                  int pair, nvfp4_dtype x_dtype);
+
+/* Synchronizes `stream` and returns, then clears, the status word of the
+ * products on the current device, all four forms: NVFP4_ERR_TIMEOUT if one of
+ * them gave up on a bounded wait since the last query (its output is then
+ * unspecified), NVFP4_OK otherwise (NVFP4_ERR_CUDA if the word could not be
+ * read).  Calls on other streams count once they have run. */
+nvfp4_status nvfp4_product_status(nvfp4_stream_t stream);
 
 /* The gated pair of a feed-forward layer in one pass:
  *   Y = silu(X Qg^T) * (X Qu^T),  silu(g) = g / (1 + exp(-g)),

@@ -119,6 +119,7 @@ def _load(path):
         "nvfp4_layer_error_workspace_size": ([i64, i64], sz),
         "nvfp4_layer_error": ([vp, i32, vp, vp, vp, vp, i64, i64, vp, vp, sz, vp], i32),
         "nvfp4_gemv_workspace_size": ([i64, i64, i64, i64, i32, i32], sz),
+        "nvfp4_product_status": ([vp], i32),
         "nvfp4_gemv": ([vp, i32, i64, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp], i32),
         "nvfp4_gemv_swiglu": ([vp, i32, i64, vp, vp, vp, vp, vp, vp, i64, i64, vp, i32, vp, sz, vp],
                               i32),
@@ -757,6 +758,12 @@ def _product(call, X, weights, Y, offsets, rows, ws, stream):
             nws)
 
 
+def nvfp4_product_status(stream=None) -> int:
+    """Waits for the stream; the first error that a product met on the current
+    device since the last query (a timed-out wait: its Y is unspecified)."""
+    return int(lib().nvfp4_product_status(_stream(stream)))
+
+
 def nvfp4_gemv(X, codes, scales, global_scale, Y, ws=None, stream=None):
     """Y (n_tok x d_out) = X (n_tok x d_in) Q^T from the codes as solved; X and
     Y each bf16 or fp32.  ws: nvfp4_gemv_workspace_size bytes
@@ -788,6 +795,12 @@ def nvfp4_gemv_swiglu_experts(X, offsets, gate, up, Y, rows=None, ws=None, strea
     if offsets is None:
         _need(call, offsets, "offsets")
     _product(call, X, [("gate ", gate), ("up ", up)], Y, offsets, rows, ws, stream)
+
+
+def product_status(device, stream=None):
+    """nvfp4_product_status of a device (its current stream unless given)."""
+    with torch.cuda.device(device):
+        return nvfp4_product_status(stream)
 
 
 def on_stream(stream):

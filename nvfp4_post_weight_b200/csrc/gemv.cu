@@ -566,6 +566,10 @@ size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, in
   return product_fp4_ws_bytes(n_rows, d_in);
 }
 
+nvfp4_status nvfp4_product_status(nvfp4_stream_t stream) {
+  return static_cast<nvfp4_status>(product_fp4_take_status(as_cuda(stream)));
+}
+
 nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const uint8_t* codes,
                         const uint8_t* scales, const float* global_scale, int64_t d_out,
                         int64_t d_in, void* Y, nvfp4_dtype y_dtype, void* ws, size_t ws_bytes,

@@ -30,6 +30,7 @@ bool product_fp4_shape(int64_t n_rows, int64_t d_in);
 size_t product_fp4_ws_bytes(int64_t n_rows, int64_t d_in);
 bool product_fp4_supported(const Product& p);
 nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st);
+int product_fp4_take_status(cudaStream_t st);
 
 // Passes over expert e's rows, `tokens` at a time (offsets are cut to
 // 0..n_rows), and its first row and their number.

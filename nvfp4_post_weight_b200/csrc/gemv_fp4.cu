@@ -260,8 +260,13 @@ struct Shared {
   int abort;
 };
 
+// The first timeout of any call since the host last asked: kept beside the calls' own
+// words, which go with their workspaces.
+__device__ int g_product_status;
+
 __device__ __forceinline__ void give_up(Shared* sh, int* status) {
   atomicExch(&sh->abort, 1);
+  atomicCAS(&g_product_status, 0, (int)NVFP4_ERR_TIMEOUT);
   pdl_wait();   // (the kernel before this one clears the word)
   atomicCAS(status, 0, (int)NVFP4_ERR_TIMEOUT);
 }
@@ -883,6 +888,22 @@ int panels_of(int64_t d_in) { return (int)(d_in / kPanelK); }
 
 bool product_fp4_shape(int64_t n_rows, int64_t d_in) {
   return d_in % kPanelK == 0 && d_in > 0 && n_rows > 0 && n_rows <= kMaxRows;
+}
+
+int product_fp4_take_status(cudaStream_t st) {
+  int v = 0, zero = 0;
+  // (cleared only where there is something to clear: what another stream's call records
+  // meanwhile stays for the next query)
+  if (cudaMemcpyFromSymbolAsync(&v, g_product_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess ||
+      (v != 0 && (cudaMemcpyToSymbolAsync(g_product_status, &zero, sizeof(int), 0,
+                                          cudaMemcpyHostToDevice, st) != cudaSuccess ||
+                  cudaStreamSynchronize(st) != cudaSuccess))) {
+    cudaGetLastError();
+    return (int)NVFP4_ERR_CUDA;
+  }
+  return v;
 }
 
 size_t product_fp4_ws_bytes(int64_t n_rows, int64_t d_in) {

@@ -193,6 +193,11 @@ class DecoderLayerSolver:
         event("hst").record(self._hst)
         st.wait_event(event("hst"))
 
+    def product_status(self, stream=None):
+        """First error of the products that this device ran since the last query (6: a
+        wait timed out and an answer is unspecified); waits for the stream."""
+        return B.product_status(self.device, stream)
+
     def status(self, stream=None):
         return (B.nvfp4_workspace_status(self.ws_prep, stream),
                 B.nvfp4_workspace_status(self.ws_quant, stream),
@@ -305,6 +310,11 @@ class MoELayerSolver:
                 Y = torch.empty_like(X)
             B.nvfp4_moe_combine(out, position, Y, weights)
         return Y
+
+    def product_status(self, stream=None):
+        """First error of the products that this device ran since the last query (6: a
+        wait timed out and an answer is unspecified); waits for the stream."""
+        return B.product_status(self.device, stream)
 
     def status(self, stream=None):
         """(prepare, quantize, layer-error, Hessian status): the first non-OK

@@ -122,6 +122,11 @@ class LayerSolver:
         if out_host is not None:
             st.wait_event(self._d2h_done)
 
+    def product_status(self, stream=None):
+        """First error of the products that this device ran since the last query (6: a
+        wait timed out and an answer is unspecified); waits for the stream."""
+        return B.product_status(self.device, stream)
+
     def status(self, stream=None):
         """Device status words of the prepare and quantize workspaces."""
         return (B.nvfp4_workspace_status(self.ws_prep, stream),

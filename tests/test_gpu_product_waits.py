@@ -5,6 +5,8 @@ import pytest
 import torch
 
 from nvfp4_post_weight_b200 import binding as B
+from nvfp4_post_weight_b200.decoder import DecoderLayerSolver, MoELayerSolver
+from nvfp4_post_weight_b200.layer import LayerSolver
 from test_gpu_gemv import BF16, DEV, F32, acts, by_expert, close, fp4, gated_fp4, sums_fp4, weights
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +63,35 @@ def test_no_copy_outlives_its_cta(monkeypatch, op, n, d_out, d_in, debug):
         by_expert(lambda r, m: close(y[r], *sums_fp4(x[r], m)), offsets, w[0])
     else:
         close(y, *(gated_fp4 if pair else sums_fp4)(x, *w))
+
+
+def test_the_solvers_tell_of_a_timed_out_product():
+    """Their products take workspaces that go with the call; the word that
+    product_status reads stays."""
+    layer = LayerSolver(40003, 512, DEV)
+    dec = DecoderLayerSolver((("x", {"gate": (20011, 512), "up": (20011, 512)}),), DEV)
+    moe = MoELayerSolver(8, 2560, 2048, DEV)
+    for codes, scales, sg in ((layer.codes, layer.scales, layer.s_g), dec.weight("gate"),
+                              dec.weight("up"), *moe.stacked.values()):
+        c, s, g = weights((*sg.shape[:codes.dim() - 2], codes.shape[-2], 2 * codes.shape[-1]), 5)
+        codes.copy_(c), scales.copy_(s), sg.copy_(g)
+    x = acts(5, 512, BF16, 3) * 0.1
+    xm = acts(5, 2560, BF16, 4) * 0.1
+    ids = torch.arange(10, dtype=torch.int32, device=DEV).view(5, 2) % 8
+    w = torch.rand((5, 2), device=DEV)
+    assert fp4(5, 40003, 512) and fp4(5, 20011, 512, 0, True) and fp4(10, 2048, 2560, 8, True)
+    calls = ((layer, lambda: layer.linear(x)), (dec, lambda: dec.gated("gate", "up", x)),
+             (moe, lambda: moe.forward(xm, ids, w)))
+    B.nvfp4_product_status()   # (what other tests timed out)
+    for s, call in calls:
+        good = call()
+        assert s.product_status() == 0
+        with no_waiting():
+            call()
+        assert s.product_status() == TIMEOUT
+        assert s.product_status() == 0          # read and cleared
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            again = call()
+        assert s.product_status(side) == 0 and torch.equal(good, again)
