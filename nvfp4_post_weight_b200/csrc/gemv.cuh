@@ -20,6 +20,7 @@ struct Product {
   const float* sg[2];
   void* Y;
   int64_t n_x, n_rows, n_experts, d_out, d_in;
+  int64_t row0;         // the sorted row that rows, Y and (without rows) X begin with
   int nb;               // blocks of 16 per weight row
   int n_w;              // matrices
   int x_bf16, y_bf16;   // else fp32
@@ -32,12 +33,12 @@ bool product_fp4_supported(const Product& p);
 nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st);
 int product_fp4_take_status(cudaStream_t st);
 
-// Passes over expert e's rows, `tokens` at a time (offsets are cut to
-// 0..n_rows), and its first row and their number.
+// Passes over expert e's rows, `tokens` at a time (offsets are cut to the call's
+// n_rows from row0 on), and its first row, from row0, and their number.
 __device__ __forceinline__ int expert_passes(const Product& p, int e, int tokens, int* r0, int* n) {
-  const int most = (int)p.n_rows;
-  *r0 = min(max(__ldg(p.offsets + e), 0), most);
-  *n = max(min(max(__ldg(p.offsets + e + 1), 0), most) - *r0, 0);
+  const int first = (int)p.row0, end = (int)(p.row0 + p.n_rows);
+  *r0 = min(max(__ldg(p.offsets + e), first), end) - first;
+  *n = max(min(max(__ldg(p.offsets + e + 1), first), end) - first - *r0, 0);
   return (*n + tokens - 1) / tokens;
 }
 

@@ -67,7 +67,9 @@ struct Roles {
                        kMmaWarp = kCodeWarp + 1, kDigitWarp = kMmaWarp + 1,
                        kThreads = (kDigitWarp + 1) * 32;
 };
-constexpr int64_t kMaxRows = 2048;                // sorted rows that are taken apart at a time
+// Sorted rows that are taken apart at a time: more go in as many equal parts as it
+// takes, one after another in one workspace (four bytes an entry).
+constexpr int64_t kMaxRows = 2048;
 constexpr int kTile = 128;
 constexpr int kSplitCols = 6144;                  // least columns of K that are shared out
 constexpr int kUnit = 8;                          // output columns that are shared out together
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(kDigitThreads)
   const int d_in = (int)p.d_in;
   const int64_t row = x_row(p, r);
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(p.X) + row * d_in;
-  if (r == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
+  if (p.row0 + r == 0 && blockIdx.y == 0 && threadIdx.x == 0) *status = 0;
   // the row's largest magnitude (bits order like values; not finite: above all), and the
   // exponents of the largest of every eight entries that are not all zero, summed, and
   // their number
@@ -887,7 +889,7 @@ int panels_of(int64_t d_in) { return (int)(d_in / kPanelK); }
 }  // namespace
 
 bool product_fp4_shape(int64_t n_rows, int64_t d_in) {
-  return d_in % kPanelK == 0 && d_in > 0 && n_rows > 0 && n_rows <= kMaxRows;
+  return d_in % kPanelK == 0 && d_in > 0 && n_rows > 0;
 }
 
 int product_fp4_take_status(cudaStream_t st) {
@@ -907,7 +909,7 @@ int product_fp4_take_status(cudaStream_t st) {
 }
 
 size_t product_fp4_ws_bytes(int64_t n_rows, int64_t d_in) {
-  const size_t rows = n_rows, n = panels_of(d_in);
+  const size_t rows = n_rows < kMaxRows ? n_rows : kMaxRows, n = panels_of(d_in);
   return kWsHeader + align256(rows * sizeof(int)) + align256(rows * mask_stride(n) * 2) +
          align256(rows * n * 16) + rows * n * 1024;
 }
@@ -920,7 +922,7 @@ bool product_fp4_supported(const Product& p) {
   return ok;
 }
 
-nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
+static nvfp4_status launch_part(const Product& p, void* ws, cudaStream_t st) {
   Fp4Args a;
   memset(&a, 0, sizeof(a));
   a.p = p;
@@ -1024,6 +1026,23 @@ nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
   cfg.numAttrs = a.split > 1 ? 2 : 1;
   NVFP4_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a));
   count_launches(2);
+  return NVFP4_OK;
+}
+
+nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st) {
+  const int64_t parts = (p.n_rows + kMaxRows - 1) / kMaxRows;
+  const int64_t rows = (p.n_rows + parts - 1) / parts;
+  for (int64_t r = 0; r < p.n_rows; r += rows) {
+    Product q = p;
+    q.row0 = r;
+    q.n_rows = p.n_rows - r < rows ? p.n_rows - r : rows;
+    if (p.rows)
+      q.rows = p.rows + r;
+    else
+      q.X = static_cast<const char*>(p.X) + r * p.d_in * (int64_t)sizeof(__nv_bfloat16);
+    q.Y = static_cast<char*>(p.Y) + r * p.d_out * (p.y_bf16 ? 2 : 4);
+    if (nvfp4_status s = launch_part(q, ws, st)) return s;
+  }
   return NVFP4_OK;
 }
 
