@@ -461,31 +461,46 @@ nvfp4_status launch_general(const Product& p, int* status, cudaStream_t st) {
 
 // Whether the FP4 path is the faster one.  It starts with a launch of its own and walks
 // all of K, or half, one stage after another, however few rows a CTA has; the general
-// kernel slices K further, but decodes.  So for one matrix or pair both are estimated,
-// in columns of K that the general kernel decodes: its CTA's slice with some 300 for
-// each start, times what more tokens cost it, less where its CTAs do not fill the SMs,
-// against 1100 and a sixth of K or, from 32 tokens on, four tenths.  Measured, us, FP4
-// / general, one token and 32: 1024 x 8192: 14.7 / 6.2 and 24.6 / 13.6; 8192 x 2048:
+// kernel slices K further, but decodes, and once for every 32 tokens.  So for one matrix
+// or pair both are estimated, in columns of K that the general kernel decodes: its
+// CTA's slice with some 300 for each start and pass, times what more tokens cost it,
+// less where its CTAs do not fill the SMs, against 1100 and a sixth of K or, from 32
+// tokens on, four tenths (its further passes lie beside one another).  Measured, us,
+// FP4 / general, one token and 32: 1024 x 8192: 14.7 / 6.2 and 24.6 / 13.6; 8192 x 2048:
 // 8.9 / 6.8 and 15.3 / 14.2; 8192 x 8192: 16.7 / 15.4 and 26.9 / 35.1; 4096 x 28672:
 // 26.0 / 23.3; 5120 x 12288: 18.0 / 20.7 and 31.4 / 48.1; 10240 x 8192: 17.5 / 23.3 and
-// 30.7 / 56.0; the pair of 4096 x 8192: 17.6 / 15.6 and 22.8 / 33.4.
-// By expert it also has to find its rows, so the bytes of the experts' codes decide,
-// the more rows they have the sooner: 8 pairs of 768 x 2048 (13 MB), 4, 16 and 64 rows
-// each 14.2 / 11.6, 16.9 / 15.1 and 39.9 / 52.6; 8 of 4096 x 1536 (25 MB), one row and 16
-// each 15.6 / 13.6 and 19.3 / 21.8; 8 pairs of 1536 x 4096 (50 MB), one row each 19.7 /
-// 25.2.  n_experts 0: one matrix or pair.
+// 30.7 / 56.0; the pair of 4096 x 8192: 17.6 / 15.6 and 22.8 / 33.4.  33, 65, 256 and 2048
+// tokens: 1024 x 8192: 21.0 / 20.4, 22.2 / 30.6, 44 / 87 and 166 / 699; 1024 x 1024: 11.8 /
+// 11.9, 12.7 / 18.4, 21 / 51 and 48 / 388; 4096 x 4096: 17.7 / 21.8, 18.4 / 32.7, 49 / 88 and
+// 217 / 686; the pair of 8192 x 8192: 32 / 101, 61 / 161, 151 / 487 and 1394 / 4650.
+// By expert it also has to find its rows.  The general kernel's CTAs are one per tile,
+// slice and expert, and decode a small expert in no time: 512 of 128 x 1024 (64 KB), 2 and
+// 16 rows each 50 / 23 and 163 / 49; 256 pairs of 256 x 512 (128 KB) 29 / 21 and 77 / 49; 64
+// pairs of 256 x 1024 (256 KB), 8 and 32 rows 22 / 25 and 42 / 39.  With larger ones the bytes
+// of the experts' codes decide, the more rows they have the sooner: 8 pairs of 768 x 2048
+// (13 MB), 4, 8 and 16 rows each 14.7 / 11.8, 15.5 / 19.8 and 16.7 / 25.7; 8 of 4096 x 1536 (25
+// MB), 1, 2 and 8 rows 15.9 / 14.3, 14.3 / 14.6 and 18.0 / 26.6; 16 of 2048 x 1024 (17 MB), 4 and
+// 8 rows 13.9 / 12.9 and 16.7 / 21.6; 8 pairs of 1536 x 4096 (50 MB), one row 19.9 / 25.7; 128
+// pairs of 768 x 2048 (200 MB), 1 and 64 rows 52 / 73 and 271 / 528.  And few experts of many
+// rows leave SMs to the passes: one of 1024 x 1024, 256 and 1024 rows 21 / 51 and 53 / 196; 8 of
+// 64 x 256, 256 rows each 36 / 75 (but 64 pairs of 64 x 512, 256 rows each 254 / 108).
+// n_experts 0: one matrix or pair.
 bool fp4_path(int64_t n_rows, int64_t d_out, int64_t d_in, int64_t n_experts, int n_w,
               nvfp4_dtype xt) {
   if (xt != NVFP4_BF16 || !product_fp4_shape(n_rows, d_in)) return false;
   const Division v = divide(n_rows, d_out, d_in, n_experts, n_w);
+  const int64_t ctas = v.tiles * v.slices * v.slots;
   if (n_experts > 0) {
-    const double bytes = (double)(n_w * v.slots) * (double)d_out * (double)d_in / 2;
-    return bytes * cbrt((double)(n_rows / v.slots)) >= 40e6;
+    const double rows = (double)n_rows / (double)v.slots;
+    if (rows >= 128. && 2 * ctas < kSms) return true;
+    const double each = (double)n_w * (double)d_out * (double)d_in / 2;
+    const double bytes = each * (double)v.slots;
+    return each >= 300e3 && (bytes * cbrt(rows) >= 40e6 || (rows >= 6. && bytes >= 12e6));
   }
-  const int64_t ctas = v.tiles * v.slices;
   const double waves = (double)((ctas + v.wave - 1) / v.wave);
-  const double decode = v.nt == 1 ? 1. : v.nt == 2 ? 1.5 : 2.6 * (double)((n_rows + 31) / 32);
-  double general = waves * ((double)d_in / v.slices * n_w * decode + 300.);
+  const double passes = v.nt == 4 ? (double)((n_rows + 31) / 32) : 1.;
+  const double decode = v.nt == 1 ? 1. : v.nt == 2 ? 1.5 : 2.6 * passes;
+  double general = waves * ((double)d_in / v.slices * n_w * decode + 300. * passes);
   if (ctas < kSms) general *= 0.5 + 0.5 * (double)ctas / kSms;
   const double more = n_rows <= 8 ? 0. : (double)((n_rows < 32 ? n_rows : 32) - 8);
   return general >= 1100. + (0.17 + 0.01 * more) * (double)d_in;

@@ -233,3 +233,27 @@ def test_a_weight_is_three_tensors(w):
     with pytest.raises(B.Nvfp4Error, match="expected \\(codes, scales, global_scale\\)") as e:
         B._weight("nvfp4_gemv_swiglu", "gate ", w, (), 16, 32, 0)
     assert e.value.code == ARG
+
+
+# (rows, d_out, d_in, experts, pair): whether the FP4 tensor cores were measured a fifth
+# or more faster than the decoding kernel, or slower
+PATHS = [((1, 1024, 8192, 0, False), False), ((32, 1024, 8192, 0, False), False),
+         ((65, 1024, 8192, 0, False), True), ((96, 1024, 1024, 0, False), True),
+         ((96, 256, 1024, 0, False), True), ((32, 256, 1024, 0, False), False),
+         ((65, 2048, 2048, 0, False), True), ((2049, 1024, 1024, 0, False), True),
+         ((8192, 256, 1024, 0, False), True), ((32, 8192, 8192, 0, False), True),
+         ((512, 128, 1024, 512, False), False), ((1024, 128, 1024, 512, False), False),
+         ((8192, 128, 1024, 512, False), False), ((32768, 128, 1024, 256, False), False),
+         ((4096, 256, 512, 256, True), False), ((16384, 512, 512, 512, False), False),
+         ((8192, 128, 128, 1024, False), False), ((8192, 256, 512, 128, False), False),
+         ((16384, 64, 512, 64, True), False), ((64, 768, 2048, 8, True), True),
+         ((128, 768, 2048, 8, True), True), ((32, 768, 2048, 8, True), False),
+         ((128, 2048, 1024, 16, False), True), ((192, 768, 768, 32, True), True),
+         ((64, 256, 1024, 64, True), False), ((8192, 768, 2048, 128, True), True),
+         ((8, 1536, 4096, 8, True), True), ((1024, 1024, 1024, 1, False), True),
+         ((8192, 64, 256, 8, False), True), ((8192, 4096, 2304, 8, False), True)]
+
+
+@pytest.mark.parametrize("sizes,path", PATHS)
+def test_the_faster_kernel_is_chosen(sizes, path):
+    assert (B.nvfp4_gemv_workspace_size(*sizes) > 0) == path
