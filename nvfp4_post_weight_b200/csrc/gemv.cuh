@@ -50,9 +50,13 @@ __device__ __forceinline__ bool find_pass(const Product& p, int tokens, int slot
   if (!p.offsets) {
     const int count = (int)((p.n_rows + tokens - 1) / tokens);
     *e = 0;
-    *t0 = slot < count ? slot * tokens : count;
-    *n = min((int)p.n_rows - slot * tokens, tokens);
-    return slot < count;
+    if (slot >= count) {
+      *t0 = count;
+      return false;
+    }
+    *t0 = slot * tokens;
+    *n = min((int)p.n_rows - *t0, tokens);
+    return true;
   }
   const int lane = threadIdx.x & 31;
   int before = 0;
