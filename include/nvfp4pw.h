@@ -514,7 +514,9 @@ size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, in
  * products on the current device, all four forms: NVFP4_ERR_TIMEOUT if one of
  * them gave up on a bounded wait since the last query (its output is then
  * unspecified), NVFP4_OK otherwise (NVFP4_ERR_CUDA if the word could not be
- * read).  Calls on other streams count once they have run. */
+ * read).  Calls on other streams count once they have run.  In the debug build
+ * also NVFP4_ERR_BOUNDS of products without a workspace and of the routing
+ * calls below. */
 nvfp4_status nvfp4_product_status(nvfp4_stream_t stream);
 
 /* The gated pair of a feed-forward layer in one pass:
@@ -632,13 +634,13 @@ long long nvfp4_launch_count(void);
 
 /* Debugging support (the paper has no counterpart; it stands in for a memory
  * checker).  The library is also built as libnvfp4pw_debug.so with
- * NVFP4_DEBUG defined: there the kernels of the solve, and of the products
- * that take a workspace, check the tile and index arithmetic they derive
- * from the call's shapes (a tile decomposition that
+ * NVFP4_DEBUG defined: there every kernel checks the tile and index
+ * arithmetic it derives from the call's shapes (a tile decomposition that
  * leaves its output, a row or column past the array) before each access; a
  * failed check skips the access and records NVFP4_ERR_BOUNDS in the call's
  * status word (for the tensor-core Hessian: the status nvfp4_hessian_status
- * reads).  Results are otherwise identical to the release build.  Returns 1
+ * reads; for products without a workspace and the routing calls: the one that
+ * nvfp4_product_status reads).  Results are otherwise identical to the release build.  Returns 1
  * in the debug build, 0 in the release build.  Host-only; never fails. */
 int nvfp4_debug_build(void);
 

@@ -88,12 +88,34 @@ struct ProfileScope {
 // Debug-build check (NVFP4_DEBUG): true when cond holds; otherwise records
 // NVFP4_ERR_BOUNDS in *status (first error wins) and yields false, so that
 // the caller skips the access.  In the release build it is the constant true.
+// NVFP4_CHECK_WORD defines such a word for the kernels of one module whose calls
+// have none.
 #ifdef NVFP4_DEBUG
 #define NVFP4_DCHECK(cond, status)                                                  \
   ((cond) ? true : (atomicCAS((status), 0, (int)NVFP4_ERR_BOUNDS), false))
+#define NVFP4_CHECK_WORD(name) static __device__ int name
+#define NVFP4_TAKE_WORD(name, st) take_status_word(name, st)
 #else
 #define NVFP4_DCHECK(cond, status) true
+#define NVFP4_CHECK_WORD(name)
+#define NVFP4_TAKE_WORD(name, st) ((void)(st), 0)
 #endif
+
+// Reads a module's status word (a __device__ int) and clears it where it was set:
+// what another stream's call records meanwhile stays for the next query.
+inline int take_status_word(const int& word, cudaStream_t st) {
+  int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbolAsync(&v, word, sizeof(int), 0, cudaMemcpyDeviceToHost, st) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess ||
+      (v != 0 && (cudaMemcpyToSymbolAsync(word, &zero, sizeof(int), 0, cudaMemcpyHostToDevice,
+                                          st) != cudaSuccess ||
+                  cudaStreamSynchronize(st) != cudaSuccess))) {
+    cudaGetLastError();
+    return (int)NVFP4_ERR_CUDA;
+  }
+  return v;
+}
 
 #define NVFP4_LAUNCH_CHECK()                                   \
   do {                                                         \
@@ -181,6 +203,10 @@ nvfp4_status launch_hessian_tc_group(int P, float* const* H, const void* const* 
                                      const int64_t* n_tok, int64_t d, int beta,
                                      cudaStream_t st);
 int hessian_tc_take_status(cudaStream_t st);
+// The products' and the routing kernels' words (the last two: debug build checks).
+int product_fp4_take_status(cudaStream_t st);
+int product_general_take_status(cudaStream_t st);
+int route_take_status(cudaStream_t st);
 
 // TMA descriptors of the tensor-core trailing update: Delta = Dh + Dl
 // (d_out x 128, fp32 each) and the split rows U = Uh + Ul of one batch,

@@ -39,6 +39,17 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+NVFP4_CHECK_WORD(g_check);
+#ifdef NVFP4_DEBUG
+// Debug build: `bytes` at p lie in the launch's dynamic shared memory, which begins at base.
+__device__ __forceinline__ bool in_smem(const void* base, const void* p, int64_t bytes) {
+  uint32_t size;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(size));
+  const int64_t at = static_cast<const char*>(p) - static_cast<const char*>(base);
+  return at >= 0 && at + bytes <= (int64_t)size;
+}
+#endif
+
 constexpr int kWarps = 8;
 constexpr int kRowsCta = 16 * kWarps;
 constexpr int kChunk = 128;                   // K per step: 64 bytes of codes a row
@@ -139,6 +150,10 @@ __device__ __forceinline__ void stage_tokens(const Product& a, int64_t t0, int n
     const int at = ((u >> 4) * n + tok) * 16 +
                    ((((u & 3) << 2) | ((u >> 2) & 3)) ^ ((tok & 1) << 2));
     const bool ok = k < a.d_in && r >= 0 && r < a.n_x;   // (d_in is a multiple of 8)
+    if (!NVFP4_DCHECK(at < plane && t0 + tok < a.n_rows &&
+                          in_smem(xs, xs + (sizeof(TX) == 2 ? 0 : 2) * plane + at, 16),
+                      &g_check))
+      continue;
     if constexpr (sizeof(TX) == 2) {
       uint4 v = make_uint4(0, 0, 0, 0);
       if (ok) v = __ldg(reinterpret_cast<const uint4*>(X + r * a.d_in + k));
@@ -200,7 +215,8 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
   for (int m = 0; m < NW; ++m)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int64_t r = (int64_t)e * a.d_out + min(row + g + 8 * h, a.d_out - 1);
+      int64_t r = (int64_t)e * a.d_out + min(row + g + 8 * h, a.d_out - 1);
+      if (!NVFP4_DCHECK(r >= 0 && r < a.n_experts * a.d_out, &g_check)) r = 0;
       codes[m][h] = a.codes[m] + r * nb * 8;
       scales[m][h] = a.scales[m] + r * nb;
     }
@@ -263,7 +279,7 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
 #pragma unroll
               for (int pl = 0; pl < kPlanes; ++pl) {
                 uint4 b = make_uint4(0, 0, 0, 0);
-                if (tok < n)
+                if (tok < n && NVFP4_DCHECK(((c - c0) * n + tok) * 16 + 16 <= plane, &g_check))
                   b = xs[pl * plane + ((c - c0) * n + tok) * 16 + ((4 * w + t) ^ ((tok & 1) << 2))];
 #pragma unroll
                 for (int m = 0; m < NW; ++m) {
@@ -305,15 +321,16 @@ __global__ void __launch_bounds__(256, NT * NW > 4 ? 1 : 2) product_kernel(const
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int tok = 8 * nt + 2 * t + (i & 1);
-          if (tok < n)
-            part[(m * max_tok + tok) * kRowsCta + warp * 16 + g + 8 * (i >> 1)] = tot[m][nt][i];
+          float* at = part + (m * max_tok + tok) * kRowsCta + warp * 16 + g + 8 * (i >> 1);
+          if (tok < n && NVFP4_DCHECK(in_smem(smem, at, 4), &g_check)) *at = tot[m][nt][i];
         }
     cluster.sync();
     // each CTA joins and writes its share of the columns
     const int share = kRowsCta / S;
     for (int i = threadIdx.x; i < n * share; i += blockDim.x) {
       const int tok = i / share, col = rank * share + i - tok * share;
-      if (o0 + col < a.d_out) {
+      if (o0 + col < a.d_out &&
+          NVFP4_DCHECK(col < kRowsCta && t0 + tok < a.n_rows && n <= max_tok, &g_check)) {
         float v[NW];
 #pragma unroll
         for (int m = 0; m < NW; ++m) {
@@ -566,6 +583,9 @@ nvfp4_status product(const void* X, nvfp4_dtype xt, int64_t n_x, const int* rows
 }
 
 }  // namespace
+
+int product_general_take_status(cudaStream_t st) { return NVFP4_TAKE_WORD(g_check, st); }
+
 }  // namespace nvfp4
 
 using namespace nvfp4;
@@ -582,7 +602,12 @@ size_t nvfp4_gemv_workspace_size(int64_t n_rows, int64_t d_out, int64_t d_in, in
 }
 
 nvfp4_status nvfp4_product_status(nvfp4_stream_t stream) {
-  return static_cast<nvfp4_status>(product_fp4_take_status(as_cuda(stream)));
+  cudaStream_t st = as_cuda(stream);
+  const int words[3] = {product_fp4_take_status(st), product_general_take_status(st),
+                        route_take_status(st)};
+  for (int w : words)
+    if (w != 0) return static_cast<nvfp4_status>(w);
+  return NVFP4_OK;
 }
 
 nvfp4_status nvfp4_gemv(const void* X, nvfp4_dtype x_dtype, int64_t n_tok, const uint8_t* codes,

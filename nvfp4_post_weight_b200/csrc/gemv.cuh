@@ -31,7 +31,6 @@ bool product_fp4_shape(int64_t n_rows, int64_t d_in);
 size_t product_fp4_ws_bytes(int64_t n_rows, int64_t d_in);
 bool product_fp4_supported(const Product& p);
 nvfp4_status launch_product_fp4(const Product& p, void* ws, cudaStream_t st);
-int product_fp4_take_status(cudaStream_t st);
 
 // Passes over expert e's rows, `tokens` at a time (offsets are cut to the call's
 // n_rows from row0 on), and its first row, from row0, and their number.

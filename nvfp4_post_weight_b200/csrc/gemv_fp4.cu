@@ -195,7 +195,8 @@ __global__ void __launch_bounds__(kDigitThreads)
   const int E = exponent(big);
   if (blockIdx.y == 0 && threadIdx.x == 0) expo[r] = finite ? E : kNonFinite;
   const int k = blockIdx.y * kDigitCols + threadIdx.x * 8;
-  const bool in = k < d_in;   // (warp-uniform: whole panels)
+  // (warp-uniform: whole panels)
+  const bool in = k < d_in && NVFP4_DCHECK(k + 8 <= d_in && r < p.n_rows, status);
   float f[8] = {};
   if (in && row >= 0 && finite) load8(x + k, f);
   uint32_t most = largest(f);
@@ -540,6 +541,19 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
 
   Pieces pieces;
   pieces.init(a, kSplit);
+#ifdef NVFP4_DEBUG
+  // what the launch laid out fits: the other CTA's sums and the ring (with the rows behind
+  // a short tile) into shared memory, sums and scales into tensor memory
+  uint32_t smem_size;
+  asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(smem_size));
+  const int64_t end = stages + (int64_t)S * a.stage_bytes + (kTile - a.tile) * (128 + 16 * P) - smem_raw;
+  if (!NVFP4_DCHECK(end <= (int64_t)smem_size && S <= kMaxStages && a.sf_bufs <= S &&
+                        a.tile <= kTile && sfb_at + ((P - 1) * a.tokens + 16 * blocks) * 16 <= a.stage_bytes &&
+                        a.d_bufs * NW * columns + a.sf_bufs * sf_cols <= kTmemCols &&
+                        (kSplit == 1 || a.tokens * NW * kTile * 4 <= a.part_bytes),
+                    a.status))
+    pieces.u = pieces.u_end;
+#endif
   Piece q;
   int s = 0;          // slot of shared memory and its phase
   uint32_t ph = 0;
@@ -892,21 +906,7 @@ bool product_fp4_shape(int64_t n_rows, int64_t d_in) {
   return d_in % kPanelK == 0 && d_in > 0 && n_rows > 0;
 }
 
-int product_fp4_take_status(cudaStream_t st) {
-  int v = 0, zero = 0;
-  // (cleared only where there is something to clear: what another stream's call records
-  // meanwhile stays for the next query)
-  if (cudaMemcpyFromSymbolAsync(&v, g_product_status, sizeof(int), 0, cudaMemcpyDeviceToHost, st) !=
-          cudaSuccess ||
-      cudaStreamSynchronize(st) != cudaSuccess ||
-      (v != 0 && (cudaMemcpyToSymbolAsync(g_product_status, &zero, sizeof(int), 0,
-                                          cudaMemcpyHostToDevice, st) != cudaSuccess ||
-                  cudaStreamSynchronize(st) != cudaSuccess))) {
-    cudaGetLastError();
-    return (int)NVFP4_ERR_CUDA;
-  }
-  return v;
-}
+int product_fp4_take_status(cudaStream_t st) { return take_status_word(g_product_status, st); }
 
 size_t product_fp4_ws_bytes(int64_t n_rows, int64_t d_in) {
   const size_t rows = n_rows < kMaxRows ? n_rows : kMaxRows, n = panels_of(d_in);

@@ -20,6 +20,8 @@
 namespace nvfp4 {
 namespace {
 
+NVFP4_CHECK_WORD(g_check);
+
 // ---- the sort ----------------------------------------------------------------
 // Placing a warp's 32 slots in order takes about 60 cycles of its SM (the warp's
 // match and the counters), counting them by shared atomics less.  Up to 4096 slots
@@ -56,8 +58,8 @@ __device__ __forceinline__ void count_slots(const void* ids, int wide, int64_t s
 // Gives one warp's slots [s0, s1) their rows in order: next (shared) holds the
 // row where the warp's next slot of each expert goes.
 __device__ __forceinline__ void place_slots(const void* ids, int wide, int64_t s0, int64_t s1,
-                                            int n_experts, int top_k, int* next, int32_t* rows,
-                                            int32_t* position) {
+                                            int64_t n, int n_experts, int top_k, int* next,
+                                            int32_t* rows, int32_t* position) {
   const int lane = threadIdx.x & 31;
   for (int64_t b = s0; b < s1; b += 32) {
     const int64_t s = b + lane;
@@ -69,7 +71,7 @@ __device__ __forceinline__ void place_slots(const void* ids, int wide, int64_t s
     __syncwarp();
     if (e < n_experts && before == 0) next[e] = r + __popc(same);
     __syncwarp();
-    if (s < s1) {
+    if (s < s1 && NVFP4_DCHECK(s >= 0 && s < n && r < n, &g_check)) {
       position[s] = r;
       if (r >= 0) rows[r] = (int32_t)(s / top_k);
     }
@@ -163,9 +165,10 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   scan_totals(tot, n_experts, warp_sums, offsets);
   counts_to_rows(cnt, n_experts, tot);
   __syncthreads();
-  place_slots(ids, wide, w0, w1, n_experts, top_k, mine, rows, position);
+  place_slots(ids, wide, w0, w1, n, n_experts, top_k, mine, rows, position);
   // the rows behind the last expert's (the CTA's own write, read after a barrier)
   const int64_t kept = n_experts > 0 ? offsets[n_experts] : 0;
+  if (!NVFP4_DCHECK(kept >= 0 && kept <= n, &g_check)) return;
   for (int64_t r = kept + threadIdx.x; r < n; r += blockDim.x) rows[r] = -1;
 }
 
@@ -182,7 +185,8 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   warp_range(s0, s1, &w0, &w1);
   count_slots(ids, wide, w0, w1, n_experts, cnt);
   __syncthreads();
-  for (int e = threadIdx.x; e < n_experts; e += blockDim.x) position[s0 + e] = cnt[e];
+  for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
+    if (NVFP4_DCHECK(s0 + e < s1 && s1 <= n, &g_check)) position[s0 + e] = cnt[e];
 }
 
 // One CTA: chunk counts -> each chunk's first row of each expert, and offsets.
@@ -196,7 +200,9 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   pdl_wait();
   const int e = threadIdx.x % n_experts, part = threadIdx.x / n_experts;
   const int per = (n_chunks + parts - 1) / parts;
-  const int c0 = min(part * per, n_chunks), c1 = part < parts ? min(c0 + per, n_chunks) : c0;
+  const int c0 = min(part * per, n_chunks);
+  int c1 = part < parts ? min(c0 + per, n_chunks) : c0;
+  if (!NVFP4_DCHECK(n_experts <= chunk && c1 <= n_chunks, &g_check)) c1 = c0;
   int s = 0;
 #pragma unroll 8
   for (int c = c0; c < c1; ++c) s += position[c * chunk + e];
@@ -232,12 +238,14 @@ __global__ void __launch_bounds__(kSortWarps * 32)
   int* mine = cnt + (threadIdx.x >> 5) * n_experts;
   count_slots(ids, wide, w0, w1, n_experts, mine);
   pdl_wait();
-  for (int e = threadIdx.x; e < n_experts; e += blockDim.x) first[e] = position[s0 + e];
+  for (int e = threadIdx.x; e < n_experts; e += blockDim.x)
+    if (NVFP4_DCHECK(s0 + e < s1 && s1 <= n, &g_check)) first[e] = position[s0 + e];
   __syncthreads();   // every thread has its counts: the positions may be written
   counts_to_rows(cnt, n_experts, first);
   __syncthreads();
-  place_slots(ids, wide, w0, w1, n_experts, top_k, mine, rows, position);
+  place_slots(ids, wide, w0, w1, n, n_experts, top_k, mine, rows, position);
   const int64_t kept = offsets[n_experts];
+  if (!NVFP4_DCHECK(kept >= 0 && kept <= n, &g_check)) return;
   for (int64_t r = kept + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < n;
        r += (int64_t)gridDim.x * blockDim.x)
     rows[r] = -1;
@@ -313,10 +321,12 @@ __global__ void __launch_bounds__(256)
     const int64_t c = first_column<V, kVec>(b, threadIdx.x, 256);
     if (c >= d) break;
     alignas(16) T v[V];
+    if (!NVFP4_DCHECK((t + 1) * top_k <= n_slots && (!kVec || c + V <= d), &g_check)) break;
     load_row<T, V, kVec, 256>(X + t * d, c, d, v);
     for (int j = 0; j < top_k; ++j) {
       const int64_t p = position[t * top_k + j];
-      if (p >= 0 && p < n_slots) store_row<T, V, kVec, 256>(Xs + p * d, c, d, v);
+      if (p >= 0 && p < n_slots && NVFP4_DCHECK(!kVec || c + V <= d, &g_check))
+        store_row<T, V, kVec, 256>(Xs + p * d, c, d, v);
     }
   }
 }
@@ -341,6 +351,7 @@ __global__ void __launch_bounds__(256)
         p[j] = j0 + j < top_k ? position[t * top_k + j0 + j] : -1;
         if (p[j] >= n_slots) p[j] = -1;
         if (kVec) y[j] = {};   // (else the loads wait for the positions: 92 us)
+        if (!NVFP4_DCHECK(!kVec || c + V <= d, &g_check)) p[j] = -1;
         if (p[j] >= 0) y[j].load(Ys + p[j] * d, c, d);
       }
 #pragma unroll
@@ -354,7 +365,8 @@ __global__ void __launch_bounds__(256)
     alignas(16) TY o[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = (TY)acc[i];
-    store_row<TY, V, kVec, 256>(Y + t * d, c, d, o);
+    if (NVFP4_DCHECK((t + 1) * top_k <= n_slots && (!kVec || c + V <= d), &g_check))
+      store_row<TY, V, kVec, 256>(Y + t * d, c, d, o);
   }
 }
 
@@ -377,6 +389,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll 4
     for (int64_t c = kVec ? lane * V : lane; c < d; c += 32 * V) {
       alignas(16) T g[V], y[V], o[V];
+      if (!NVFP4_DCHECK(!kVec || c + V <= d, &g_check)) break;
       load_row<T, V, kVec, 32>(dY + t * d, c, d, g);
       load_row<T, V, kVec, 32>(Ys + p * d, c, d, y);
 #pragma unroll
@@ -442,6 +455,9 @@ void launch_backward(bool vec, const void* dY, const void* Ys, const int32_t* po
 }
 
 }  // namespace
+
+int route_take_status(cudaStream_t st) { return NVFP4_TAKE_WORD(g_check, st); }
+
 }  // namespace nvfp4
 
 using namespace nvfp4;
