@@ -672,7 +672,9 @@ enum {
   NVFP4_PHASE_PANEL = 7,   /* inside PREPARE: its Cholesky panel launches  */
   NVFP4_PHASE_FACTOR_I8 = 8, /* inside PREPARE: its int8-slice GEMMs (with
                                 their slicing launches); work = fp64 flops */
-  NVFP4_NUM_PHASES = 9
+  NVFP4_PHASE_PRODUCT = 9, /* nvfp4_gemv and its other forms                */
+  NVFP4_PHASE_ROUTE = 10,  /* nvfp4_moe_sort, _gather, _combine, _backward  */
+  NVFP4_NUM_PHASES = 11
 };
 
 /* Starts a profiling window: from now on every phase above records a CUDA

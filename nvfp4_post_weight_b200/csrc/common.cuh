@@ -71,6 +71,7 @@ enum Phase {
   kPhaseRoute = 10,
   kNumPhases = 11
 };
+static_assert(kPhaseRoute == NVFP4_PHASE_ROUTE && kNumPhases == NVFP4_NUM_PHASES, "public phases");
 // While profiling is on, adds algorithmic work (flops) to the open phase.
 void add_phase_work(double work);
 // Adds n to the library's kernel-launch counter (and to the open phase's).

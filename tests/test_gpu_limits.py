@@ -90,3 +90,25 @@ def test_products_of_several_threads(dtype):
                                              None, 0, st.cuda_stream)
 
     assert together(*[products(n) for n in (32, 24, 30, 25)], times=10000) == []
+
+
+def test_phases_of_products_and_routing():
+    """The profile's phases, by the public header's numbers."""
+    import ctypes
+    import re
+    src = open(os.path.join(ROOT, "include", "nvfp4pw.h")).read()
+    phase = {m[0]: int(m[1]) for m in re.findall(r"NVFP4_(\w+) = (\d+)", src)}
+    n = phase["NUM_PHASES"]
+    ms, launches = (ctypes.c_double * n)(), (ctypes.c_longlong * n)()
+    i32 = dict(dtype=torch.int32, device=DEV)
+    ids, off, rows, pos = (torch.zeros(s, **i32) for s in ((4, 2), (4,), (8,), (4, 2)))
+    x, y = torch.ones((4, 32), device=DEV), torch.empty((4, 16), device=DEV)
+    w = (torch.zeros((16, 16), dtype=torch.uint8, device=DEV),
+         torch.zeros((16, 2), dtype=torch.uint8, device=DEV), torch.ones(1, device=DEV))
+    assert B.lib().nvfp4_profile_begin() == 0
+    B.nvfp4_gemv(x, *w, y)
+    B.nvfp4_moe_sort(ids, off, rows, pos)
+    B.nvfp4_moe_gather(x, pos, torch.empty((8, 32), device=DEV))
+    assert B.lib().nvfp4_profile_end(ms, launches, n) == 0
+    assert launches[phase["PHASE_PRODUCT"]] == 1 and launches[phase["PHASE_ROUTE"]] == 2
+    assert ms[phase["PHASE_PRODUCT"]] > 0 and ms[phase["PHASE_ROUTE"]] > 0
