@@ -103,8 +103,7 @@ struct Fp4Args {
 // CTA (r, part): sorted row r (zeros if it points outside X), 4096 columns.
 constexpr int kDigitThreads = 512, kDigitCols = kDigitThreads * 8;
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
   const uint32_t h[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -144,12 +143,11 @@ __device__ __forceinline__ float scaled(float f, int e) {
 // Entries of a row of block masks: one per panel, and zeros up to whole 16-byte words.
 __host__ __device__ constexpr int mask_stride(int n_panels) { return (n_panels + 7) / 8 * 8; }
 
-// Magnitude bits of the largest of eight entries.
-__device__ __forceinline__ uint32_t largest(const float* f) {
-  uint32_t most = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) most = max(most, __float_as_uint(f[j]) & 0x7FFFFFFFu);
-  return most;
+// Magnitude bits (of fp32) of the largest of eight entries, compared two at a time.
+__device__ __forceinline__ uint32_t largest(const uint4& v) {
+  constexpr uint32_t kBits = 0x7FFF7FFFu;
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & kBits, v.y & kBits), __vmaxu2(v.z & kBits, v.w & kBits));
+  return max(m << 16, m & 0xFFFF0000u);
 }
 
 __global__ void __launch_bounds__(kDigitThreads)
@@ -172,9 +170,7 @@ __global__ void __launch_bounds__(kDigitThreads)
   if (row >= 0)
 #pragma unroll 4
     for (int k = threadIdx.x * 8; k < d_in; k += kDigitThreads * 8) {
-      float f[8];
-      load8(x + k, f);
-      const uint32_t most = largest(f);
+      const uint32_t most = largest(__ldg(reinterpret_cast<const uint4*>(x + k)));
       big = max(big, most);
       if (most) sum += exponent(most), ++count;
     }
@@ -197,9 +193,11 @@ __global__ void __launch_bounds__(kDigitThreads)
   const int k = blockIdx.y * kDigitCols + threadIdx.x * 8;
   // (warp-uniform: whole panels)
   const bool in = k < d_in && NVFP4_DCHECK(k + 8 <= d_in && r < p.n_rows, status);
-  float f[8] = {};
-  if (in && row >= 0 && finite) load8(x + k, f);
-  uint32_t most = largest(f);
+  uint4 entries = make_uint4(0, 0, 0, 0);
+  if (in && row >= 0 && finite) entries = __ldg(reinterpret_cast<const uint4*>(x + k));
+  float f[8];
+  unpack8(entries, f);
+  uint32_t most = largest(entries);
   most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));   // a block is two lanes' entries
   const int below = min(E - exponent(most), 17);
   const int up = 27 - (E - below);
