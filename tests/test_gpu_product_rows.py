@@ -128,3 +128,23 @@ def test_nonfinite_tokens_of_pairs_and_experts(pair):
             assert torch.equal(got[inf], ref[inf])
             assert not (torch.isfinite(ref).any() and not pair)
     by_expert(check, offsets, *ws_)
+
+
+@pytest.mark.parametrize("E,d_out,n", [(1, 8, 700), (3, 13, 900), (2, 130, 2500)])
+@pytest.mark.parametrize("pair", [False, True])
+def test_few_experts_of_many_rows(E, d_out, n, pair):
+    """Few columns: few CTAs in the general kernel, so the passes go to this one."""
+    d_in = 512
+    assert fp4(n, d_out, d_in, E, pair)
+    ws_ = [weights((E, d_out, d_in), s) for s in ((5, 6) if pair else (5,))]
+    x = acts(n, d_in, BF16, 9) * 0.1
+    ends = torch.arange(E + 1) * (n - 7) // E
+    offsets = (ends + 3).int().to(DEV)      # three rows before the first expert's
+    y = torch.full((n, d_out), 7.0, device=DEV)
+    if pair:
+        B.nvfp4_gemv_swiglu_experts(x, offsets, *ws_, y)
+    else:
+        B.nvfp4_gemv_experts(x, offsets, *ws_[0], y)
+    fn = gated_fp4 if pair else sums_fp4
+    by_expert(lambda r, *m: close(y[r], *fn(x[r], *m)), offsets, *ws_)
+    assert (y[:3] == 7).all() and (y[n - 4:] == 7).all()
