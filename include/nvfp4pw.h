@@ -484,13 +484,13 @@ nvfp4_status nvfp4_dequant_batched(int count, const uint8_t* const* codes,
  * scales are 16-byte aligned: there a (bf16) token's entry is kept to 2^-28 of
  * the largest of its block of 16 columns, or to 2^-45 of the token's largest
  * where that is more (entries within 2^-20 of their block's largest are
- * exact), and never to less than 2^-20 of 2^m, m the mean exponent of the
- * largest of every eight entries, all zeros aside: what would be lost beyond
- * that, beside outliers, is added in a second step of some 4 us a token and a
- * CTA's 128 columns.  Elsewhere tokens are used at all their bits.  NaN and
- * infinite tokens behave as in the plain product and stay in their row (there
- * by plain sums that are slow: eight such tokens through 8192 x 28672 take 20
- * ms, where others take 36 us); tokens beyond
+ * exact), and to 2^-20 of 2^m at least, m the mean exponent of the largest of
+ * every eight entries, all zeros aside: what more would be lost, beside large
+ * outliers, is added in a second step (some 4 us a token and tile of columns).
+ * Elsewhere tokens are used at all their bits.  NaN and infinite tokens behave
+ * as in the plain product and stay in their row, on the FP4 tensor cores by
+ * plain sums that are slow (eight such tokens through 8192 x 28672 take 20 ms,
+ * eight others 36 us); tokens beyond
  * 2^120 may overflow on the way, and scale code 127 (a NaN, which the quantize
  * call does not write) may give any value in its column.  Made for few tokens,
  * where the weights' bytes bound the product; any n_tok is right, but from some
@@ -634,8 +634,9 @@ long long nvfp4_launch_count(void);
 
 /* Debugging support (the paper has no counterpart; it stands in for a memory
  * checker).  The library is also built as libnvfp4pw_debug.so with
- * NVFP4_DEBUG defined: there every kernel checks the tile and index
- * arithmetic it derives from the call's shapes (a tile decomposition that
+ * NVFP4_DEBUG defined: there the tensor-core kernels of the solve and the
+ * kernels of the products and of the routing check the tile and index
+ * arithmetic they derive from the call's shapes (a tile decomposition that
  * leaves its output, a row or column past the array) before each access; a
  * failed check skips the access and records NVFP4_ERR_BOUNDS in the call's
  * status word (for the tensor-core Hessian: the status nvfp4_hessian_status

@@ -289,9 +289,12 @@ nvfp4_status launch_layer_error_group(int P, const PtrArr<const void*>& W, nvfp4
 // access; it returns once the previous kernel of the stream has completed and
 // its writes are visible.  The launch itself and the set-up before the wait
 // (barrier init, tensor-map prefetch, TMEM allocation) overlap the previous
-// kernel's completion.  No kernel triggers its dependents early: measured on
-// the 4096-wide layer, CTAs of the next kernel parked beside a running panel
-// or GEMM slowed it more than the earlier start gained.
+// kernel's completion.  No kernel of the solve triggers its dependents early:
+// measured on the 4096-wide layer, CTAs of the next kernel parked beside a running
+// panel or GEMM slowed it more than the earlier start gained.  The digits' kernel of
+// the products (gemv_fp4.cu) does, at its start, and the product reads offsets, codes
+// and scales before its wait: they are what the digits' launch, an ordinary one, has
+// waited for already, and only what the digits' kernel writes comes after the wait.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... KArgs, typename... Args>

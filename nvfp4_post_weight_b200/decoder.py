@@ -89,12 +89,12 @@ class DecoderLayerSolver:
 
     def linear(self, name, X, Y=None, stream=None):
         """Y = X Q^T for a few tokens X from the solved codes of a tensor; Y of
-        X's dtype unless given."""
+        X's dtype unless given.  No gradient is recorded."""
         return B.into(Y, X, self.shapes[name][0], stream, B.nvfp4_gemv, X, *self.weight(name))
 
     def gated(self, gate, up, X, Y=None, stream=None):
         """Y = silu(X Qg^T) * (X Qu^T) from two solved tensors of one shape, the
-        input of the down projection."""
+        input of the down projection.  No gradient is recorded."""
         return B.into(Y, X, self.shapes[gate][0], stream, B.nvfp4_gemv_swiglu, X,
                       self.weight(gate), self.weight(up))
 
@@ -297,7 +297,8 @@ class MoELayerSolver:
         down_e(silu(gate_e x_t) * up_e x_t), e = expert_ids[t, j] (a slot whose
         id is outside the experts adds nothing).  X n_tok x hidden, weights
         n_tok x top_k fp32; Y of X's dtype unless given.  The intermediate is
-        rounded to X's dtype, the experts' answers are fp32."""
+        rounded to X's dtype, the experts' answers are fp32.  No gradient is
+        recorded: binding.nvfp4_moe_combine_backward has the one of the weights."""
         with B.on_stream(stream):
             offsets, rows, position = self.sort(expert_ids)
             n, dev = expert_ids.numel(), X.device

@@ -57,7 +57,7 @@ class LayerSolver:
 
     def linear(self, X, Y=None, stream=None):
         """Y = X Q^T for a few tokens X (n_tok x d_in, bf16 or fp32) from the
-        solved codes; Y of X's dtype unless given."""
+        solved codes; Y of X's dtype unless given.  No gradient is recorded."""
         return B.into(Y, X, self.d_out, stream, B.nvfp4_gemv, X, self.codes, self.scales, self.s_g)
 
     def step(self, W, X, stream=None, with_error=True):
