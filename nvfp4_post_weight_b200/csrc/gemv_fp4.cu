@@ -608,7 +608,9 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
       return fmaf(high, 28561.f, low);
     };
     auto value = [&](float sum, int E, int w) {
-      return (double)sum * (__hiloint2double((E - 34 + 1023) << 20, 0) * (double)sg[w]);
+      // (what a token of the second loop gives here, its E not being one, is written over)
+      const double power = __hiloint2double((int)((uint32_t)(E - 34 + 1023) << 20), 0);
+      return (double)sum * (power * (double)sg[w]);
     };
     // two sums at a time: both matrices' of a token, or one matrix' of two tokens
     constexpr int kTokens = 2 / NW;
