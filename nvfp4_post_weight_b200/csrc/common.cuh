@@ -71,7 +71,8 @@ enum Phase {
   kPhaseRoute = 10,
   kNumPhases = 11
 };
-static_assert(kPhaseRoute == NVFP4_PHASE_ROUTE && kNumPhases == NVFP4_NUM_PHASES, "public phases");
+static_assert((int)kPhaseRoute == (int)NVFP4_PHASE_ROUTE && (int)kNumPhases == (int)NVFP4_NUM_PHASES,
+              "the public header's phases");
 // While profiling is on, adds algorithmic work (flops) to the open phase.
 void add_phase_work(double work);
 // Adds n to the library's kernel-launch counter (and to the open phase's).

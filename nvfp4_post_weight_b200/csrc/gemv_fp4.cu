@@ -461,7 +461,7 @@ __device__ __noinline__ float special_product(const Fp4Args& a, int w, int e, in
   float sum = 0.f;
   for (int first = 0; first < n_panels; first += 32) {
     uint32_t mine = 0;   // the blocks of panel first + lane
-    if (first + lane < n_panels) mine = plain ? 0xFFFFu : masks[first + lane];
+    if (first + lane < n_panels) mine = plain ? 0xFFFFu : __ldca(masks + first + lane);
     for (unsigned some = __ballot_sync(~0u, mine != 0); some; some &= some - 1) {
       const int at = __ffs(some) - 1;
       for (uint32_t bits = __shfl_sync(~0u, mine, at); bits; bits &= bits - 1) {
@@ -569,15 +569,17 @@ __global__ void __launch_bounds__(Roles<NW>::kThreads, 1)
   bool any_special = false;
   float sg[NW];
   auto enter_pass = [&](const Piece& q) {
+    // (ordinary loads: the kernel before this one, which this one may have started beside,
+    // wrote them, and the read-only path wants data that nobody writes meanwhile)
     exponent = 0;
     if (lane < q.n) {
-      exponent = __ldg(a.expo + q.t0 + lane);
+      exponent = __ldca(a.expo + q.t0 + lane);
       const int words = mask_stride(a.p.nb / 16) / 8;
       const uint4* masks = reinterpret_cast<const uint4*>(a.blocks) + (int64_t)(q.t0 + lane) * words;
       uint32_t left = 0;
 #pragma unroll 4
       for (int i = 0; i < words; ++i) {
-        const uint4 m = __ldg(masks + i);
+        const uint4 m = __ldca(masks + i);
         left |= m.x | m.y | m.z | m.w;
       }
       if (left) exponent += kLeftOut;
