@@ -32,10 +32,10 @@
 // do not mix), 256 or 512 columns of K a stage.  Where few rows have many columns, two
 // CTAs share the columns: the second's sums go to the first's shared memory.
 //
-// What bounds it: one token's DRAM bytes (the 28672 x 8192 pair, 264 MB in 51 us, 80%
+// What bounds it: one token's DRAM bytes (the 28672 x 8192 pair, 264 MB in 50.2 us, 82%
 // of the copy rate); with more tokens the traffic from L2 to the SMs, where
 // every CTA reads all digits, four bytes an entry, beside its rows (the pair with
-// 32 tokens, two passes, 0.84 GB in 97 us); with few rows an SM the chain of
+// 32 tokens, two passes, 0.95 GB in 94 us); with few rows an SM the chain of
 // stages (some 0.25 us per 256 columns).  Loading scales through registers instead
 // of TMA took 58 us for the one-token pair, copies of scales by tcgen05.cp from
 // the issuing thread 95 us, a single warp lane's non-uniform loop 68 us.
